@@ -546,6 +546,82 @@ int lora_compress_export(const float *sigma, const int32_t *k, const int64_t *of
                          int64_t d_out, int32_t r, uint16_t *A_new, uint16_t *B_new, void *workspace,
                          size_t workspace_bytes, lora_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The frozen base held in 8 bits: blocks of 128, each e4m3 values (passed as
+ * bytes) on one fp32 scale, x = scale · value. Half the bytes of a bf16 base and
+ * twice its tensor-core rate; the adapters stay bf16. No counterpart in the
+ * pages (which fix no storage for the frozen W).
+ *
+ * lora_fp8_quantize_rows — activations or gradients in blocks of 1 x 128.
+ *   X  bf16 [T, d]             d a multiple of 16, >= 16; T >= 1
+ *   Q  e4m3 bytes [T, d]       16-byte aligned
+ *   S  f32 [ceil(d/128), T]    scale of block b of row t at S[b*T + t] (the rows
+ *                              of one block lie together; 4-byte aligned)
+ * lora_fp8_quantize_weight — a weight in blocks of 128 x 128.
+ *   W  bf16 [d_in, d_out]      both multiples of 16, >= 16
+ *   Q  e4m3 bytes [d_in, d_out]
+ *   S  f32 [ceil(d_in/128), ceil(d_out/128)]
+ * A block's scale is the smallest power of two >= (its largest magnitude) / 448,
+ * at least 2^-126, and 1 for a block of zeros; its values are x / scale (exact)
+ * rounded to e4m3, nearest, ties to even. A block that holds an infinity or a
+ * NaN gets the scale NaN, so every result it enters is NaN. The last block of a
+ * row or column may be short.
+ * Errors: LORA_ERR_ARG, LORA_ERR_UNSUPPORTED, LORA_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+int lora_fp8_quantize_rows(const uint16_t *X, int64_t T, int64_t d, uint8_t *Q, float *S, lora_stream_t stream);
+int lora_fp8_quantize_weight(const uint16_t *W, int64_t d_in, int64_t d_out, uint8_t *Q, float *S,
+                             lora_stream_t stream);
+
+/* lora_base_gemm_fp8 — the base product over blocks of 128, no adapter term:
+ *   transpose 0:  Y[t, n] = sum_b Sx[b, t]·Sw[b, n/128]·sum_{k in block b} Xq[t, k]·Wq[k, n]
+ *                 Xq [T, d_in], Sx [ceil(d_in/128), T], Y bf16 [T, d_out]
+ *   transpose 1:  Y = Xq·W^T from the same weight (the backward's dX = dY·W^T):
+ *                 Xq [T, d_out], Sx [ceil(d_out/128), T], Y bf16 [T, d_in]
+ *   Wq [d_in, d_out], Sw [ceil(d_in/128), ceil(d_out/128)]; d_in, d_out
+ *   multiples of 16, >= 16. Sx and Sw may hold any fp32 values (those of
+ *   lora_fp8_quantize_* or of a checkpoint).
+ * Each block's product is formed in fp32 and added, scaled, to fp32 sums; one
+ * rounding to bf16. The order of the sums is fixed: results are the same run to
+ * run. Xq, Wq, Y 16-byte aligned, Sx, Sw 4-byte aligned.
+ * Errors: LORA_ERR_ARG, LORA_ERR_UNSUPPORTED, LORA_ERR_CUDA. */
+int lora_base_gemm_fp8(const uint8_t *Xq, const float *Sx, const uint8_t *Wq, const float *Sw, uint16_t *Y, int64_t T,
+                       int64_t d_in, int64_t d_out, int transpose, lora_stream_t stream);
+
+/* lora_linear_fwd_fp8 — lora_linear_fwd over an 8-bit base: the rows of X are
+ * quantised (blocks of 1 x 128, as lora_fp8_quantize_rows) into the workspace in
+ * the plan's order, the adapter branch reads X itself, unquantised, and one
+ * kernel forms both terms: Y[t] = X̂[t]·Ŵ + s_a·((D ⊙ X)[t]·A_a)·B_a, X̂ and Ŵ the
+ * values that the quantised blocks stand for.
+ *   Wq, Sw   as in lora_base_gemm_fp8 (d_in, d_out multiples of 16)
+ *   workspace, workspace_bytes  device scratch of at least
+ *            lora_linear_fwd_fp8_workspace_size(plan) bytes (0: the plan's widths
+ *            are not multiples of 16), 256-byte aligned, caller-owned; contents
+ *            on entry are ignored
+ *   the rest as in lora_linear_fwd (the plan's scratch is used the same way)
+ * Errors: LORA_ERR_ARG, LORA_ERR_WORKSPACE, LORA_ERR_UNSUPPORTED, LORA_ERR_CUDA. */
+size_t lora_linear_fwd_fp8_workspace_size(lora_plan_t plan);
+int lora_linear_fwd_fp8(lora_plan_t plan, const uint16_t *X, const uint8_t *Wq, const float *Sw, const uint16_t *A_pool,
+                        const uint16_t *B_pool, const float *scale, double p_drop, uint64_t seed, uint16_t *Y,
+                        float *U_save, void *workspace, size_t workspace_bytes, const uint32_t *keep_bits,
+                        lora_stream_t stream);
+
+/* lora_linear_bwd_multi_fp8 — lora_linear_bwd_multi over an 8-bit base (one
+ * adapter or many: a plan of one adapter is the single-adapter backward). The
+ * base term of dX is that of dY's rows quantised in blocks of 1 x 128 along
+ * d_out, times Ŵ^T from the same Wq, Sw as the forward; the quantisation of X in
+ * the forward is taken as the identity (W is frozen, so no other gradient sees
+ * it). dA, dB and the adapter term of dX are those of lora_linear_bwd_multi, from
+ * the unquantised X and dY.
+ *   workspace  lora_linear_bwd_multi_fp8_workspace_size(plan) bytes, 256-byte aligned
+ *   the rest   as in lora_linear_bwd_multi
+ * Errors: as lora_linear_bwd_multi. */
+size_t lora_linear_bwd_multi_fp8_workspace_size(lora_plan_t plan);
+int lora_linear_bwd_multi_fp8(lora_plan_t plan, const uint16_t *X, const uint8_t *Wq, const float *Sw,
+                              const uint16_t *A_pool, const uint16_t *B_pool, const float *scale, double p_drop,
+                              uint64_t seed, const float *U_save, const uint16_t *dY, uint16_t *dX, float *dA_pool,
+                              float *dB_pool, void *workspace, size_t workspace_bytes, const uint32_t *keep_bits,
+                              lora_stream_t stream);
+
 /* Test hook: write the dropout mask the forward and backward use (dropout on
  * the LoRA-branch input, one of the small ops the LoRAFusion explainer lists in
  * section 解决什么真问题, item 1; the drop rule is the one under lora_linear_fwd).

@@ -101,6 +101,15 @@ def load_library():
         "lora_compress_allocate": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i32, _i32, _dbl, _i32, _vp, _vp, _vp, _sz,
                                                   _vp]),
         "lora_compress_export": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _sz, _vp]),
+        "lora_fp8_quantize_rows": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+        "lora_fp8_quantize_weight": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+        "lora_base_gemm_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, _vp]),
+        "lora_linear_fwd_fp8_workspace_size": (_sz, [_vp]),
+        "lora_linear_fwd_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _dbl, _u64, _vp, _vp, _vp, _sz, _vp,
+                                               _vp]),
+        "lora_linear_bwd_multi_fp8_workspace_size": (_sz, [_vp]),
+        "lora_linear_bwd_multi_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _dbl, _u64, _vp, _vp, _vp, _vp,
+                                                     _vp, _vp, _sz, _vp, _vp]),
         "lora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     }
     for name, (res, args) in sig.items():
@@ -123,6 +132,7 @@ def _ptr(t):
 _BF16 = ("bfloat16",)
 _F32 = ("float32",)
 _I32 = ("int32", "uint32")
+_FP8 = ("float8_e4m3fn", "uint8")  # e4m3 values, or their bytes
 
 
 _DTYPE_NAME = {}  # torch dtype -> its short name ("bfloat16", ...), filled as dtypes are seen
@@ -579,3 +589,96 @@ def compress_allocate(sigma, ranks, costs, policy: str, keep: float, k_floor: in
                                                  int(k_floor), _ptr(k), _ptr(off), _ptr(ws), need, _stream(stream)),
            "lora_compress_allocate")
     return k, off
+
+
+def _blocks128(d):
+    return -(-d // 128)
+
+
+def _workspace_bytes(what, workspace):
+    _args(what, ("workspace", workspace, tuple(workspace.shape) if workspace is not None else (),
+                 (str(workspace.dtype)[6:] if workspace is not None else "",), False))
+    return workspace.numel() * workspace.element_size()
+
+
+def _shape2(what, name, t):
+    if t is None or t.dim() != 2:
+        raise LoraError(-1, f"{what}: {name} must be a 2-D tensor")
+    return int(t.shape[0]), int(t.shape[1])
+
+
+def quantize_rows(X, Q, S, *, stream=None):
+    """lora_fp8_quantize_rows: X bf16 [T, d] as e4m3 values Q [T, d] in blocks of
+    1 x 128 with power-of-two scales S fp32 [ceil(d/128), T]."""
+    T, d = _shape2("lora_fp8_quantize_rows", "X", X)
+    _args("lora_fp8_quantize_rows", ("X", X, (T, d), _BF16, False), ("Q", Q, (T, d), _FP8, False),
+          ("S", S, (_blocks128(d), T), _F32, False))
+    _check(load_library().lora_fp8_quantize_rows(_ptr(X), T, d, _ptr(Q), _ptr(S), _stream(stream)),
+           "lora_fp8_quantize_rows")
+
+
+def quantize_weight(W, Q, S, *, stream=None):
+    """lora_fp8_quantize_weight: W bf16 [d_in, d_out] as e4m3 values Q in blocks of
+    128 x 128 with power-of-two scales S fp32 [ceil(d_in/128), ceil(d_out/128)]."""
+    di, do = _shape2("lora_fp8_quantize_weight", "W", W)
+    _args("lora_fp8_quantize_weight", ("W", W, (di, do), _BF16, False), ("Q", Q, (di, do), _FP8, False),
+          ("S", S, (_blocks128(di), _blocks128(do)), _F32, False))
+    _check(load_library().lora_fp8_quantize_weight(_ptr(W), di, do, _ptr(Q), _ptr(S), _stream(stream)),
+           "lora_fp8_quantize_weight")
+
+
+def base_gemm_fp8(Xq, Sx, Wq, Sw, Y, *, transpose: bool = False, stream=None):
+    """lora_base_gemm_fp8: Y bf16 = X·W (Xq [T, d_in], Y [T, d_out]) or, with
+    transpose, X·W^T (Xq [T, d_out], Y [T, d_in]) from e4m3 blocks of 128 and
+    their scales (Sx [ceil(k/128), T], Sw [ceil(d_in/128), ceil(d_out/128)])."""
+    T, k = _shape2("lora_base_gemm_fp8", "Xq", Xq)
+    di, do = _shape2("lora_base_gemm_fp8", "Wq", Wq)
+    _args("lora_base_gemm_fp8", ("Xq", Xq, (T, do if transpose else di), _FP8, False),
+          ("Sx", Sx, (_blocks128(k), T), _F32, False), ("Wq", Wq, (di, do), _FP8, False),
+          ("Sw", Sw, (_blocks128(di), _blocks128(do)), _F32, False),
+          ("Y", Y, (T, di if transpose else do), _BF16, False))
+    _check(load_library().lora_base_gemm_fp8(_ptr(Xq), _ptr(Sx), _ptr(Wq), _ptr(Sw), _ptr(Y), T, di, do,
+                                             1 if transpose else 0, _stream(stream)), "lora_base_gemm_fp8")
+
+
+def fwd_fp8_workspace_size(plan: Plan) -> int:
+    return int(load_library().lora_linear_fwd_fp8_workspace_size(plan.handle))
+
+
+def linear_fwd_fp8(plan: Plan, X, Wq, Sw, A_pool, B_pool, scale, Y, workspace, *, p_drop: float = 0.0, seed: int = 0,
+                   U_save=None, keep_bits=None, stream=None):
+    """lora_linear_fwd_fp8: the forward over an 8-bit base (Wq, Sw as in
+    base_gemm_fp8), with a workspace of fwd_fp8_workspace_size(plan) bytes."""
+    di, do, R = plan.d_in, plan.d_out, plan.pool_rows
+    _args("lora_linear_fwd_fp8", *_fwd_args(plan, X, A_pool, scale, U_save, keep_bits),
+          ("Wq", Wq, (di, do), _FP8, False), ("Sw", Sw, (_blocks128(di), _blocks128(do)), _F32, False),
+          ("B_pool", B_pool, (R, do), _BF16, False), ("Y", Y, (plan.T, do), _BF16, False))
+    nbytes = _workspace_bytes("lora_linear_fwd_fp8", workspace)
+    _check(load_library().lora_linear_fwd_fp8(plan.handle, _ptr(X), _ptr(Wq), _ptr(Sw), _ptr(A_pool), _ptr(B_pool),
+                                              _ptr(scale), float(p_drop), int(seed) & (2**64 - 1), _ptr(Y),
+                                              _ptr(U_save), _ptr(workspace), nbytes, _ptr(keep_bits),
+                                              _stream(stream)), "lora_linear_fwd_fp8")
+
+
+def bwd_multi_fp8_workspace_size(plan: Plan) -> int:
+    return int(load_library().lora_linear_bwd_multi_fp8_workspace_size(plan.handle))
+
+
+def linear_bwd_multi_fp8(plan: Plan, X, Wq, Sw, A_pool, B_pool, scale, U_save, dY, dX, dA_pool, dB_pool, workspace, *,
+                         p_drop: float = 0.0, seed: int = 0, keep_bits=None, stream=None):
+    """lora_linear_bwd_multi_fp8: linear_bwd_multi over an 8-bit base, with a
+    workspace of bwd_multi_fp8_workspace_size(plan) bytes."""
+    T, di, do, R = plan.T, plan.d_in, plan.d_out, plan.pool_rows
+    if U_save is None:
+        raise LoraError(-1, "lora_linear_bwd_multi_fp8: U_save is required")
+    _args("lora_linear_bwd_multi_fp8", *_fwd_args(plan, X, A_pool, scale, U_save, keep_bits),
+          ("Wq", Wq, (di, do), _FP8, False), ("Sw", Sw, (_blocks128(di), _blocks128(do)), _F32, False),
+          ("B_pool", B_pool, (R, do), _BF16, False), ("dY", dY, (T, do), _BF16, False),
+          ("dX", dX, (T, di), _BF16, False), ("dA_pool", dA_pool, (R, di), _F32, False),
+          ("dB_pool", dB_pool, (R, do), _F32, False))
+    nbytes = _workspace_bytes("lora_linear_bwd_multi_fp8", workspace)
+    _check(load_library().lora_linear_bwd_multi_fp8(plan.handle, _ptr(X), _ptr(Wq), _ptr(Sw), _ptr(A_pool),
+                                                    _ptr(B_pool), _ptr(scale), float(p_drop),
+                                                    int(seed) & (2**64 - 1), _ptr(U_save), _ptr(dY), _ptr(dX),
+                                                    _ptr(dA_pool), _ptr(dB_pool), _ptr(workspace), nbytes,
+                                                    _ptr(keep_bits), _stream(stream)), "lora_linear_bwd_multi_fp8")

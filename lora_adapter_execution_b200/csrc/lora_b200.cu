@@ -16,6 +16,7 @@
 #include "switch.cuh"
 #include "tsqr.cuh"
 #include "compress.cuh"
+#include "fp8.cuh"
 
 using namespace lora;
 
@@ -35,7 +36,8 @@ DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-bool qr_kernel_attributes();  // qr_api.inc
+bool qr_kernel_attributes();   // qr_api.inc
+bool fp8_kernel_attributes();  // fp8_api.inc
 
 int device_state(DeviceState **out) {
   int dev = 0;
@@ -83,6 +85,7 @@ int device_state(DeviceState **out) {
           ok &= cudaFuncSetAttribute(lora_tcontract_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      tc_smem(kTcMaxR)) == cudaSuccess;
           ok &= qr_kernel_attributes();
+          ok &= fp8_kernel_attributes();
           if (!ok) d.status = LORA_ERR_CUDA;
           for (int S = 1; ok && S <= 4; S *= 2) {
             cudaLaunchConfig_t cfg{};
@@ -1297,15 +1300,28 @@ size_t lora_linear_bwd_multi_workspace_size(lora_plan_t plan) {
   return static_cast<size_t>(bwd_multi_layout(plan->hp).total);
 }
 
-int lora_linear_bwd_multi(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const uint16_t *A_pool,
-                          const uint16_t *B_pool, const float *scale, double p_drop, uint64_t seed,
-                          const float *U_save, const uint16_t *dY, uint16_t *dX, float *dA_pool, float *dB_pool,
-                          void *workspace, size_t workspace_bytes, const uint32_t *keep_bits, lora_stream_t stream) {
-  if (!plan || !plan->dev || !X || !W || !A_pool || !B_pool || !scale || !U_save || !dY || !dX || !dA_pool ||
+namespace {
+// The 8-bit base of a backward: W in blocks of 128 and where the quantised dY goes.
+struct Fp8Base {
+  const uint8_t *Wq;
+  const float *Sw;
+};
+int fp8_bwd_dx(DeviceState *ds, const lora_plan *plan, const Fp8Base &f8, const uint16_t *dY, const uint16_t *A_pool,
+               const uint8_t *img, uint16_t *dX, uint64_t seed, uint64_t thr, float inv_keep, const uint32_t *bits,
+               uint8_t *ws, lora_stream_t stream);  // fp8_api.inc
+
+// lora_linear_bwd_multi, over the bf16 base W or, with f8 given, the 8-bit one
+// (whose quantised dY lives behind the bf16 backward's workspace).
+int bwd_multi_run(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const Fp8Base *f8, const uint16_t *A_pool,
+                  const uint16_t *B_pool, const float *scale, double p_drop, uint64_t seed, const float *U_save,
+                  const uint16_t *dY, uint16_t *dX, float *dA_pool, float *dB_pool, void *workspace,
+                  size_t workspace_bytes, size_t workspace_need, const uint32_t *keep_bits, lora_stream_t stream) {
+  const void *Wp = f8 ? static_cast<const void *>(f8->Wq) : static_cast<const void *>(W);
+  if (!plan || !plan->dev || !X || !Wp || !A_pool || !B_pool || !scale || !U_save || !dY || !dX || !dA_pool ||
       !dB_pool)
     return LORA_ERR_ARG;
   if (!on_plan_device(plan)) return LORA_ERR_ARG;
-  if (!aligned16(X) || !aligned16(W) || !aligned16(A_pool) || !aligned16(B_pool) || !aligned16(dY) ||
+  if (!aligned16(X) || !aligned16(Wp) || !aligned16(A_pool) || !aligned16(B_pool) || !aligned16(dY) ||
       !aligned16(dX) || (reinterpret_cast<uintptr_t>(U_save) & 3u) || (reinterpret_cast<uintptr_t>(dA_pool) & 3u) ||
       (reinterpret_cast<uintptr_t>(dB_pool) & 3u) || (reinterpret_cast<uintptr_t>(keep_bits) & 3u))
     return LORA_ERR_ARG;
@@ -1313,8 +1329,7 @@ int lora_linear_bwd_multi(lora_plan_t plan, const uint16_t *X, const uint16_t *W
   const HostPlan &hp = plan->hp;
   if (hp.pieces.size() > 65535) return LORA_ERR_ARG;  // one grid row of the reduction per piece
   const BwdMultiLayout Lw = bwd_multi_layout(hp);
-  if (!workspace || workspace_bytes < static_cast<size_t>(Lw.total) ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  if (!workspace || workspace_bytes < workspace_need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return LORA_ERR_WORKSPACE;
   DeviceState *ds = nullptr;
   int rc = device_state(&ds);
@@ -1381,7 +1396,10 @@ int lora_linear_bwd_multi(lora_plan_t plan, const uint16_t *X, const uint16_t *W
   // dX = dY·W^T + D ⊙ (s_a·dU·A_a^T): the fused GEMM over the plan's tiles, W^T a
   // K-major operand, the adapter blocks A_pool rows (into a second accumulator,
   // masked in the epilogue, when there is dropout)
-  {
+  if (f8) {
+    rc = fp8_bwd_dx(ds, plan, *f8, dY, A_pool, img, dX, seed, thr, inv_keep, bits, ws + Lw.total, stream);
+    if (rc != LORA_OK) return rc;
+  } else {
     CUtensorMap mdY128, mWt, mAl;
     const bool b3d = d_in % 64 == 0;
     bool ok = make_map(&mdY128, dYr, d_out, T, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) &&
@@ -1487,6 +1505,15 @@ int lora_linear_bwd_multi(lora_plan_t plan, const uint16_t *X, const uint16_t *W
     }
   }
   return launch_status();
+}
+}  // namespace
+
+int lora_linear_bwd_multi(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const uint16_t *A_pool,
+                          const uint16_t *B_pool, const float *scale, double p_drop, uint64_t seed,
+                          const float *U_save, const uint16_t *dY, uint16_t *dX, float *dA_pool, float *dB_pool,
+                          void *workspace, size_t workspace_bytes, const uint32_t *keep_bits, lora_stream_t stream) {
+  return bwd_multi_run(plan, X, W, nullptr, A_pool, B_pool, scale, p_drop, seed, U_save, dY, dX, dA_pool, dB_pool,
+                       workspace, workspace_bytes, lora_linear_bwd_multi_workspace_size(plan), keep_bits, stream);
 }
 
 }  // extern "C"
@@ -1770,3 +1797,6 @@ int lora_switch_apply(lora_switch_t sw, uint16_t *W, const uint16_t *A_pool, con
 // The batched tall-skinny QR and post-hoc compression entry points (and their
 // kernels' launch attributes, qr_kernel_attributes).
 #include "qr_api.inc"
+
+// The layer over an 8-bit frozen base (and its kernels' launch attributes).
+#include "fp8_api.inc"

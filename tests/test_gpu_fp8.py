@@ -1,0 +1,391 @@
+"""The 8-bit frozen base on the GPU: the quantiser bit for bit, the block-scaled
+product and the layer's forward and backward over it, against 64-bit values.
+
+Tolerances. An output is rounded once to bf16: half a step is 2^-8 of its value
+(torch.finfo(bfloat16).eps / 2). Before that, a block's product is summed by the
+tensor cores in fp32 (taken as 2^-21 of the sum of its terms' magnitudes: 128
+terms in four instructions, each addition good to at least 2^-23) and the KB
+blocks are added in fp32 (KB roundings of 2^-24 of the running sum, which the
+sum of the magnitudes bounds).
+"""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import lora_adapter_execution_b200 as lora
+import oracle
+from helpers import check_close, dev_bf16, host_f64
+from lora_adapter_execution_b200 import workloads as wl
+
+pytestmark = pytest.mark.gpu
+FP8 = torch.float8_e4m3fn
+
+
+def blocks(d):
+    return -(-d // 128)
+
+
+def ref_scale(amax):
+    """The definition, in 64 bits: the smallest power of two s with 448·s >= amax."""
+    amax = np.asarray(amax, dtype=np.float64)
+    out = np.ones_like(amax)
+    for i, a in np.ndenumerate(amax):
+        if not np.isfinite(a):
+            out[i] = np.nan
+        elif a > 0:
+            e = -126
+            while 448.0 * 2.0**e < a:
+                e += 1
+            out[i] = 2.0**e
+    return out
+
+
+def ref_e4m3(v):
+    """Nearest e4m3 value, ties to even, |v| <= 448."""
+    with np.errstate(invalid="ignore", divide="ignore"):
+        step = np.exp2(np.floor(np.log2(np.maximum(np.abs(v), 2.0**-6))) - 3)
+        return np.rint(v / step) * step
+
+
+def ref_rows(x):
+    T, d = x.shape
+    q, s = np.empty_like(x), np.empty((blocks(d), T))
+    for b in range(blocks(d)):
+        c = slice(128 * b, min(128 * b + 128, d))
+        s[b] = ref_scale(np.abs(x[:, c]).max(1))
+        q[:, c] = ref_e4m3(x[:, c] / s[b][:, None])
+    return q, s
+
+
+def ref_weight(w):
+    q, s = np.empty_like(w), np.empty((blocks(w.shape[0]), blocks(w.shape[1])))
+    for i in range(s.shape[0]):
+        for j in range(s.shape[1]):
+            c = np.s_[128 * i:min(128 * i + 128, w.shape[0]), 128 * j:min(128 * j + 128, w.shape[1])]
+            s[i, j] = ref_scale(np.abs(w[c]).max())
+            q[c] = ref_e4m3(w[c] / s[i, j])
+    return q, s
+
+
+def rows_value(q, s):
+    out = q.copy()
+    for b in range(s.shape[0]):
+        out[:, 128 * b:128 * b + 128] *= s[b][:, None]
+    return out
+
+
+def weight_value(q, s):
+    return q * np.repeat(np.repeat(s, 128, 0)[:q.shape[0]], 128, 1)[:, :q.shape[1]]
+
+
+def f64(t):
+    return t.to(torch.float32).double().cpu().numpy()
+
+
+def quantize_rows(X):
+    T, d = X.shape
+    # a guard row behind the values and a guard element behind the scales
+    Q = torch.full((T + 1, d), 1.5, device="cuda").to(FP8)
+    S = torch.full((blocks(d) * T + 1,), 7.0, device="cuda")
+    lora.quantize_rows(X, Q[:T], S[:-1].view(blocks(d), T))
+    assert (f64(Q[T:]) == 1.5).all() and float(S[-1]) == 7.0
+    return Q[:T], S[:-1].view(blocks(d), T)
+
+
+@pytest.mark.parametrize("T,d", [(1, 16), (1, 4096), (3, 128), (5, 144), (37, 400), (130, 1008), (257, 4112)])
+def test_quantize_rows_bit_for_bit(T, d):
+    rng = np.random.default_rng(T * 1000 + d)
+    x = rng.standard_normal((T, d)) * np.exp2(rng.integers(-60, 60, size=(T, 1)).astype(np.float64))
+    X = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    X[T // 2, : min(d, 128)] = 0.0  # a block of zeros
+    Q, S = quantize_rows(X)
+    q, s = ref_rows(f64(X))
+    assert np.array_equal(f64(S), s)
+    assert np.array_equal(f64(Q), q)
+    assert lora.device_status() == 0
+
+
+def test_quantize_values_at_the_borders():
+    """Ties, the largest value on and just over 448·2^k, subnormal scales' floor, -0, inf and NaN."""
+    d = 128
+    x = np.zeros((9, d))
+    x[0, :8] = [448, 17, 19, 21, -17, 2.0**-10, 3 * 2.0**-10, 2.0**-9]  # ties between e4m3 values
+    x[1, :3] = [450, 1, -1]          # bf16 450 > 448: the next power of two
+    x[2, :2] = [2.0**-130, 2.0**-133]  # amax below 448·2^-126: the scale's floor
+    x[3, :2] = [3.0e38, 1.0]
+    x[4, :2] = [-448.0 * 2**10, 448.0]
+    x[5, :2] = [-0.0, 0.0]
+    x[6, 5] = np.inf
+    x[7, 127] = np.nan
+    x[8, :2] = [2.0**-126 * 448, 2.0**-126]
+    X = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    Q, S = quantize_rows(X)
+    q, s = ref_rows(f64(X))
+    ok = np.r_[0:6, 8]
+    assert np.array_equal(f64(S)[:, ok], s[:, ok]) and np.array_equal(f64(Q)[ok], q[ok])
+    assert np.isnan(f64(S)[0, 6:8]).all() and np.isnan(f64(Q)[6:8]).all()
+
+
+@pytest.mark.parametrize("di,do", [(16, 16), (128, 128), (144, 400), (272, 1008), (400, 16)])
+def test_quantize_weight_bit_for_bit(di, do):
+    rng = np.random.default_rng(di + do)
+    w = rng.standard_normal((di, do)) * np.exp2(rng.integers(-3, 3, size=(di, do)).astype(np.float64))
+    W = torch.from_numpy(w).to(torch.bfloat16).cuda()
+    Q, S = torch.empty(di, do, device="cuda").to(FP8), torch.empty(blocks(di), blocks(do), device="cuda")
+    lora.quantize_weight(W, Q, S)
+    q, s = ref_weight(f64(W))
+    assert np.array_equal(f64(S), s) and np.array_equal(f64(Q), q)
+
+
+# sizes that take each tile width, the K split (1 to 8 CTAs), ragged tiles and short blocks
+SIZES = [(1, 16, 16), (1, 4096, 128), (2, 144, 272), (7, 1040, 400), (64, 256, 256), (129, 272, 1008), (200, 2064, 528),
+         (300, 128, 4096), (1000, 400, 4112), (5000, 144, 1040), (2100, 1168, 2576)]
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("T,di,do", SIZES)
+def test_product_integers_exact(T, di, do, transpose):
+    """Small integers on scales of one: every sum is an exact fp32 integer, so the
+    result is the one bf16 rounding of the exact product, bit for bit."""
+    k, n = (do, di) if transpose else (di, do)
+    g = torch.Generator(device="cuda").manual_seed(T + di + do)
+    X = torch.randint(-3, 4, (T, k), generator=g, device="cuda").float()
+    W = torch.randint(-3, 4, (di, do), generator=g, device="cuda").float()
+    Y = torch.full((T + 1, n), 5.0, dtype=torch.bfloat16, device="cuda")
+    lora.base_gemm_fp8(X.to(FP8), torch.ones(blocks(k), T, device="cuda"), W.to(FP8),
+                       torch.ones(blocks(di), blocks(do), device="cuda"), Y[:T], transpose=transpose)
+    assert lora.device_status() == 0
+    ref = (X.double() @ (W.T if transpose else W).double()).to(torch.bfloat16)
+    assert torch.equal(Y[:T], ref)
+    assert (Y[T] == 5.0).all()
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("T,di,do", SIZES)
+def test_product_any_scales(T, di, do, transpose):
+    k, n = (do, di) if transpose else (di, do)
+    g = torch.Generator(device="cuda").manual_seed(T * 7 + di + do)
+    Xq = torch.randn(T, k, generator=g, device="cuda").mul(20).clamp(-448, 448).to(FP8)
+    Wq = torch.randn(di, do, generator=g, device="cuda").mul(20).clamp(-448, 448).to(FP8)
+    Sx = torch.rand(blocks(k), T, generator=g, device="cuda") + 0.01
+    Sw = torch.rand(blocks(di), blocks(do), generator=g, device="cuda") - 0.3
+    Y = torch.empty(T, n, dtype=torch.bfloat16, device="cuda")
+    lora.base_gemm_fp8(Xq, Sx, Wq, Sw, Y, transpose=transpose)
+    assert lora.device_status() == 0
+    X = rows_value(f64(Xq), f64(Sx))
+    W = weight_value(f64(Wq), f64(Sw))
+    W = W.T if transpose else W
+    ref, mag = X @ W, np.abs(X) @ np.abs(W)
+    tol = 2.0**-8 * np.abs(ref) + (2.0**-21 + (blocks(k) + 3) * 2.0**-24) * mag
+    assert (np.abs(f64(Y) - ref) <= tol).all()
+
+
+def test_product_runs_the_same_twice_and_in_a_graph():
+    T, di, do = 33, 2048, 512
+    g = torch.Generator(device="cuda").manual_seed(1)
+    Xq = torch.randn(T, di, generator=g, device="cuda").to(FP8)
+    Wq = torch.randn(di, do, generator=g, device="cuda").to(FP8)
+    Sx, Sw = torch.rand(blocks(di), T, generator=g, device="cuda"), torch.rand(blocks(di), blocks(do), device="cuda")
+    Y, Z = (torch.empty(T, do, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lora.base_gemm_fp8(Xq, Sx, Wq, Sw, Y)
+    graph = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=s):
+        lora.base_gemm_fp8(Xq, Sx, Wq, Sw, Z)
+    for _ in range(3):
+        Z.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, Z)
+
+
+def test_nan_and_inf_stay_in_their_rows_and_blocks():
+    """A NaN in a row of X makes that row NaN; one in W makes its block's columns NaN."""
+    T, d = 40, 512
+    g = torch.Generator(device="cuda").manual_seed(2)
+    X = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+    W = torch.randn(d, d, generator=g, device="cuda").to(torch.bfloat16)
+    X[3, 200] = float("inf")
+    W[100, 300] = float("nan")
+    Xq, Sx = quantize_rows(X)
+    Wq, Sw = torch.empty(d, d, device="cuda").to(FP8), torch.empty(4, 4, device="cuda")
+    lora.quantize_weight(W, Wq, Sw)
+    Y = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    lora.base_gemm_fp8(Xq, Sx, Wq, Sw, Y)
+    bad = torch.isnan(Y).cpu().numpy()
+    want = np.zeros((T, d), bool)
+    want[3] = True
+    want[:, 256:384] = True
+    assert np.array_equal(bad, want)
+
+
+# ------------------------------------------------------------------ the layer
+def layer(T, di, do, ranks, ids, p, seed=0, with_dy=True):
+    n = len(ranks)
+    spec = wl.Spec("case", T, di, do, n, ("list", tuple(ranks)), ("uniform",), 2.0, p_drop=p, with_dy=with_dy, seed=seed)
+    inp = wl.make_inputs(spec)
+    inp.ids[:] = ids
+    return inp
+
+
+def run_layer(inp, use_bits=True, backward=True):
+    dev = "cuda"
+    plan = lora.Plan(inp.ids, inp.ranks, inp.d_in, inp.d_out)
+    X, A, B = dev_bf16(inp.X), dev_bf16(inp.A_pool), dev_bf16(inp.B_pool)
+    W = dev_bf16(inp.W)
+    Wq, Sw = torch.empty(W.shape, device=dev).to(FP8), torch.empty(blocks(inp.d_in), blocks(inp.d_out), device=dev)
+    lora.quantize_weight(W, Wq, Sw)
+    scale = torch.from_numpy(inp.scale).to(dev)
+    bits = None
+    if inp.p_drop > 0 and use_bits:
+        bits = torch.empty(inp.T, -(-inp.d_in // 32), dtype=torch.int32, device=dev)
+        lora.dropout_keep_bits(inp.mask_seed, inp.p_drop, bits, inp.d_in)
+    Y = torch.empty(inp.T, inp.d_out, dtype=torch.bfloat16, device=dev)
+    U = torch.empty(inp.T, plan.r_max, device=dev)
+    kw = dict(p_drop=inp.p_drop, seed=inp.mask_seed, keep_bits=bits)
+    ws = torch.empty(lora.fwd_fp8_workspace_size(plan), dtype=torch.uint8, device=dev)
+    lora.linear_fwd_fp8(plan, X, Wq, Sw, A, B, scale, Y, ws, U_save=U, **kw)
+    assert lora.device_status() == 0
+    out = [Y, U]
+    if backward:
+        dY = dev_bf16(inp.dY)
+        dX = torch.empty(inp.T, inp.d_in, dtype=torch.bfloat16, device=dev)
+        dA, dB = torch.zeros(A.shape, device=dev), torch.zeros(B.shape, device=dev)
+        ws = torch.empty(lora.bwd_multi_fp8_workspace_size(plan), dtype=torch.uint8, device=dev)
+        lora.linear_bwd_multi_fp8(plan, X, Wq, Sw, A, B, scale, U, dY, dX, dA, dB, ws, **kw)
+        assert lora.device_status() == 0
+        out += [dX, dA, dB]
+    plan.destroy()
+    return out
+
+
+def ref_layer(inp):
+    b = wl.bf16_bits_to_f32
+    X, W, A, B, dY = (b(v).astype(np.float64) for v in (inp.X, inp.W, inp.A_pool, inp.B_pool, inp.dY))
+    W = weight_value(*ref_weight(W))
+    keep = 1.0
+    if inp.p_drop > 0:
+        keep = (1 - oracle.mask(inp.mask_seed, inp.p_drop, inp.T, inp.d_in)) / (1 - inp.p_drop)
+    Y = rows_value(*ref_rows(X)) @ W
+    dX = rows_value(*ref_rows(dY)) @ W.T
+    dA, dB = np.zeros(A.shape), np.zeros(B.shape)
+    Xd = X * keep
+    for a in range(inp.n_adapters):
+        t = np.flatnonzero(inp.ids == a)
+        r = slice(int(inp.offsets[a]), int(inp.offsets[a + 1]))
+        s = float(inp.scale[a])
+        U = Xd[t] @ A[r].T
+        Y[t] += s * U @ B[r]
+        dU = s * dY[t] @ B[r].T
+        low = dU @ A[r]
+        dX[t] += low * (keep[t] if inp.p_drop > 0 else 1.0)
+        dA[r], dB[r] = dU.T @ Xd[t], s * U.T @ dY[t]
+    return Y, dX, dA, dB
+
+
+LAYERS = [
+    # T, d_in, d_out, ranks, ids, p: one token; a single adapter; ranks off 16; many small runs; wide tiles
+    (1, 256, 272, [5], lambda T: 0, 0.0),
+    (40, 144, 400, [16], lambda T: 0, 0.1),
+    (64, 256, 256, [4, 8, 8, 16], lambda T: np.arange(T) % 4, 0.1),
+    (200, 400, 272, [1, 21, 64, 33], lambda T: (np.arange(T) // 50) % 4, 0.0),
+    (300, 1040, 656, list(range(1, 22)), lambda T: (np.arange(T) * 7) % 21, 0.1),
+    (130, 256, 512, [256, 3], lambda T: (np.arange(T) > 100).astype(np.int32), 0.1),
+    (2600, 656, 2064, [8, 16, 32], lambda T: (np.arange(T) // 512) % 3, 0.0),
+    (2600, 2064, 656, [8, 13, 32], lambda T: (np.arange(T) * 5) % 3, 0.1),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LAYERS)))
+def test_layer_forward_and_backward(case):
+    T, di, do, ranks, ids, p = LAYERS[case]
+    inp = layer(T, di, do, ranks, ids(T), p, seed=case)
+    Y, U, dX, dA, dB = run_layer(inp)
+    rY, rdX, rdA, rdB = ref_layer(inp)
+    check_close(host_f64(Y), rY, "Y")
+    check_close(host_f64(dX), rdX, "dX")
+    check_close(host_f64(dA), rdA, "dA")
+    check_close(host_f64(dB), rdB, "dB")
+
+
+def test_layer_mask_from_the_generator_equals_the_bits():
+    inp = layer(200, 400, 272, [5, 16], np.arange(200) % 2, 0.3, seed=4)
+    for a, b in zip(run_layer(inp, True), run_layer(inp, False)):
+        assert torch.equal(a, b)
+
+
+def test_layer_shares_its_adapter_branch_with_the_bf16_layer():
+    """U_save, dA and dB are those of the bf16 layer, bit for bit: the 8-bit base does not touch them."""
+    inp = layer(300, 256, 512, [7, 16, 40], (np.arange(300) * 5) % 3, 0.1, seed=5)
+    _, U8, _, dA8, dB8 = run_layer(inp)
+    plan = lora.Plan(inp.ids, inp.ranks, inp.d_in, inp.d_out)
+    X, W, A, B, dY = (dev_bf16(v) for v in (inp.X, inp.W, inp.A_pool, inp.B_pool, inp.dY))
+    scale = torch.from_numpy(inp.scale).cuda()
+    Y = torch.empty(inp.T, inp.d_out, dtype=torch.bfloat16, device="cuda")
+    U = torch.empty(inp.T, plan.r_max, device="cuda")
+    kw = dict(p_drop=inp.p_drop, seed=inp.mask_seed)
+    lora.linear_fwd(plan, X, W, A, B, scale, Y, U_save=U, **kw)
+    dX = torch.empty(inp.T, inp.d_in, dtype=torch.bfloat16, device="cuda")
+    dA, dB = torch.zeros(A.shape, device="cuda"), torch.zeros(B.shape, device="cuda")
+    ws = torch.empty(lora.bwd_multi_workspace_size(plan), dtype=torch.uint8, device="cuda")
+    lora.linear_bwd_multi(plan, X, W, A, B, scale, U, dY, dX, dA, dB, ws, **kw)
+    assert torch.equal(U, U8) and torch.equal(dA, dA8) and torch.equal(dB, dB8)
+    plan.destroy()
+
+
+def test_gradient_of_the_input_against_differences():
+    """dX against central differences of L = sum(Y·G) along random directions, on
+    an input and gradient that e4m3 holds exactly: the layer is then linear in X
+    between the two points, which e4m3 holds too, and only roundings remain. Y is
+    rounded to bf16 (2^-8 of each element), so L is off by at most
+    2^-8 · sum |Y||G| at each point, and the difference by twice that over 2h = 2."""
+    T, di, do, r = 24, 256, 128, 8
+    rng = np.random.default_rng(6)
+    dev = "cuda"
+    ints = lambda *s, lo=-4, hi=5: torch.from_numpy(rng.integers(lo, hi, size=s).astype(np.float32)).to(dev)
+    X, D, G = ints(T, di), ints(T, di, lo=-1, hi=2), ints(T, do)
+    X[:, ::128] = 8.0  # every block of every point has the largest value 8 or 9: one scale throughout
+    D[:, ::128] = 0.0
+    W, A, B = ints(di, do), ints(r, di, lo=-1, hi=2), ints(r, do, lo=-1, hi=2)
+    plan = lora.Plan(np.zeros(T, np.int32), np.array([r], np.int32), di, do)
+    bf = torch.bfloat16
+    Wq, Sw = W.to(FP8), torch.ones(blocks(di), blocks(do), device=dev)
+    scale = torch.ones(1, device=dev)
+    ws = torch.empty(max(lora.fwd_fp8_workspace_size(plan), lora.bwd_multi_fp8_workspace_size(plan)), dtype=torch.uint8,
+                     device=dev)
+
+    def loss(x):
+        Y = torch.empty(T, do, dtype=bf, device=dev)
+        U = torch.empty(T, r, device=dev)
+        lora.linear_fwd_fp8(plan, x.to(bf), Wq, Sw, A.to(bf), B.to(bf), scale, Y, ws, U_save=U)
+        return (Y.double() * G.double()).sum().item(), (Y.double() * G.double()).abs().sum().item(), U
+
+    lp, mp, _ = loss(X + D)
+    lm, mm, _ = loss(X - D)
+    _, _, U = loss(X)
+    dX = torch.empty(T, di, dtype=bf, device=dev)
+    dA, dB = torch.empty(r, di, device=dev), torch.empty(r, do, device=dev)
+    lora.linear_bwd_multi_fp8(plan, X.to(bf), Wq, Sw, A.to(bf), B.to(bf), scale, U, G.to(bf), dX, dA, dB, ws)
+    want = (lp - lm) / 2
+    got = (dX.double() * D.double()).sum().item()
+    tol = 2.0**-8 * ((mp + mm) / 2 + (dX.double() * D.double()).abs().sum().item())
+    assert abs(got - want) <= tol
+    plan.destroy()
+
+
+def test_layer_two_streams_two_plans():
+    """Two calls at once, each with its own plan and workspace, equal the calls one after the other."""
+    inps = [layer(150 + 50 * i, 512, 384, [8, 16], np.arange(150 + 50 * i) % 2, 0.0, seed=7 + i) for i in range(2)]
+    alone = [run_layer(i, backward=False) for i in inps]
+    streams = [torch.cuda.Stream() for _ in inps]
+    got = []
+    for s, i in zip(streams, inps):
+        with torch.cuda.stream(s):
+            got.append(run_layer(i, backward=False))
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
