@@ -622,6 +622,51 @@ int lora_linear_bwd_multi_fp8(lora_plan_t plan, const uint16_t *X, const uint8_t
                               float *dB_pool, void *workspace, size_t workspace_bytes, const uint32_t *keep_bits,
                               lora_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Muon over a pool of adapter factors: the optimiser's step for the gradients
+ * that lora_linear_bwd_multi writes, every adapter's factor a matrix of its own
+ * (adapter a's rows off_a .. off_a + r_a - 1 of a pool [R, d]: A_pool or B_pool).
+ * No counterpart in the pages (they fix no optimiser). For each adapter:
+ *   m'  = beta·m + (1 - beta)·g
+ *   u   = (1 - beta)·g + beta·m'  (nesterov 1)  or  m'
+ *   X0  = u / (|u|_F + 1e-7)
+ *   X  <- 3.4445·X + (-4.7750·A + 2.0315·A·A)·X,  A = X·X^T,  five times: O
+ *   w'  = (1 - lr·weight_decay)·w - lr·gain·O,  gain = rms·sqrt(max(r_a, d)) (rms > 0) or 1 (rms 0)
+ *   pool = bf16(w')
+ * The Gram matrix and the products of r x r matrices are kept in 64 bits, the
+ * d-long rows in fp32. The results do not depend on which other adapters the
+ * context holds, and are the same run to run.
+ *
+ * lora_muon_create — a context for pools of one shape.
+ *   ranks_host  int32[n_adapters]: 1 .. LORA_MAX_RANK
+ *   d           the rows' length, a multiple of 8, >= 8 (d_in for A_pool, d_out for B_pool)
+ * It owns device tables and scratch, copies them to the device (the call waits
+ * for that) and belongs to the device current at this call. Two calls with one
+ * context must be ordered (they share its scratch), two captured graphs' replays
+ * included.
+ * lora_muon_orthogonalize — O f32 [R, d] of u = U f32 [R, d]; O must not overlap U.
+ * lora_muon_step — the step. grad, momentum, master f32 [R, d] in, momentum_out,
+ *   master_out f32 [R, d] out, pool bf16 [R, d] out or NULL. momentum_out may be
+ *   momentum and master_out may be master (in place); no output may overlap
+ *   anything else. beta in [0, 1); lr, weight_decay, rms >= 0; nesterov 0 or 1.
+ *   active  int32 [n_adapters] DEVICE or NULL (all): adapters with active[a] = 0
+ *           are left out, no output row of theirs is written (adapters without
+ *           tokens in the batch, whose gradient rows the backward leaves as they
+ *           were)
+ * All arrays 16-byte aligned (active 4). Rows are read and written in fp32; a
+ * non-finite value in an adapter's rows makes that adapter's results NaN, no other's.
+ * Errors: LORA_ERR_ARG, LORA_ERR_RANK, LORA_ERR_NOMEM, LORA_ERR_UNSUPPORTED, LORA_ERR_CUDA.
+ * ------------------------------------------------------------------------ */
+typedef struct lora_muon *lora_muon_t;
+
+int lora_muon_create(const int32_t *ranks_host, int32_t n_adapters, int64_t d, lora_muon_t *out);
+int lora_muon_orthogonalize(lora_muon_t mu, const float *U, float *O, const int32_t *active, lora_stream_t stream);
+int lora_muon_step(lora_muon_t mu, const float *grad, const float *momentum, const float *master, float *momentum_out,
+                   float *master_out, uint16_t *pool, double lr, double beta, int nesterov, double weight_decay,
+                   double rms, const int32_t *active, lora_stream_t stream);
+/* Free the context (the caller must not free one that queued work still uses). NULL is ignored. */
+void lora_muon_destroy(lora_muon_t mu);
+
 /* Test hook: write the dropout mask the forward and backward use (dropout on
  * the LoRA-branch input, one of the small ops the LoRAFusion explainer lists in
  * section 解决什么真问题, item 1; the drop rule is the one under lora_linear_fwd).

@@ -12,4 +12,4 @@ from .abi import (LoraError, Plan, base_gemm, bwd_workspace_size, device_status,
                   fused_gemm, linear_bwd, linear_bwd_static, linear_fwd, linear_fwd_host, linear_shrink, load_library,
                   selftest_bounded_wait, tsqr, tsqr_workspace_size, Compressor,
                   compress_allocate, quantize_rows, quantize_weight, base_gemm_fp8, linear_fwd_fp8,
-                  fwd_fp8_workspace_size, linear_bwd_multi_fp8, bwd_multi_fp8_workspace_size)
+                  fwd_fp8_workspace_size, linear_bwd_multi_fp8, bwd_multi_fp8_workspace_size, Muon)

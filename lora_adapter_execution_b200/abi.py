@@ -110,6 +110,11 @@ def load_library():
         "lora_linear_bwd_multi_fp8_workspace_size": (_sz, [_vp]),
         "lora_linear_bwd_multi_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _dbl, _u64, _vp, _vp, _vp, _vp,
                                                      _vp, _vp, _sz, _vp, _vp]),
+        "lora_muon_create": (ctypes.c_int, [_vp, _i32, _i64, ctypes.POINTER(_vp)]),
+        "lora_muon_orthogonalize": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp]),
+        "lora_muon_step": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _dbl, _dbl, ctypes.c_int, _dbl, _dbl, _vp,
+                                          _vp]),
+        "lora_muon_destroy": (None, [_vp]),
         "lora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     }
     for name, (res, args) in sig.items():
@@ -682,3 +687,53 @@ def linear_bwd_multi_fp8(plan: Plan, X, Wq, Sw, A_pool, B_pool, scale, U_save, d
                                                     int(seed) & (2**64 - 1), _ptr(U_save), _ptr(dY), _ptr(dX),
                                                     _ptr(dA_pool), _ptr(dB_pool), _ptr(workspace), nbytes,
                                                     _ptr(keep_bits), _stream(stream)), "lora_linear_bwd_multi_fp8")
+
+
+class Muon:
+    """Muon's step for pools of adapter factors of the given ranks and row length d
+    (lora_muon_create); one context serves every pool of that shape, calls in order."""
+
+    def __init__(self, ranks, d: int):
+        self._ranks = _host_i32(ranks)
+        self.d, self.n_adapters = int(d), int(self._ranks.shape[0])
+        self.pool_rows = int(self._ranks.astype(np.int64).sum())
+        h = _vp()
+        _check(load_library().lora_muon_create(self._ranks.ctypes.data_as(_vp), self.n_adapters, self.d,
+                                               ctypes.byref(h)), "lora_muon_create")
+        self._h = h
+
+    def orthogonalize(self, U, O, *, active=None, stream=None):
+        """O fp32 [R, d]: each adapter's rows of U fp32 [R, d] through five Newton-Schulz steps."""
+        R, d = self.pool_rows, self.d
+        _args("lora_muon_orthogonalize", ("U", U, (R, d), _F32, False), ("O", O, (R, d), _F32, False),
+              ("active", active, (self.n_adapters,), _I32, True))
+        _check(load_library().lora_muon_orthogonalize(self._h, _ptr(U), _ptr(O), _ptr(active), _stream(stream)),
+               "lora_muon_orthogonalize")
+
+    def step(self, grad, momentum, master, momentum_out=None, master_out=None, pool=None, *, lr: float,
+             beta: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0, rms: float = 0.2, active=None,
+             stream=None):
+        """One step: momentum and master fp32 [R, d] from grad fp32 [R, d] (in place
+        where no outputs are given), the updated weights as bf16 in pool [R, d]."""
+        R, d = self.pool_rows, self.d
+        momentum_out = momentum if momentum_out is None else momentum_out
+        master_out = master if master_out is None else master_out
+        _args("lora_muon_step", ("grad", grad, (R, d), _F32, False), ("momentum", momentum, (R, d), _F32, False),
+              ("master", master, (R, d), _F32, False), ("momentum_out", momentum_out, (R, d), _F32, False),
+              ("master_out", master_out, (R, d), _F32, False), ("pool", pool, (R, d), _BF16, True),
+              ("active", active, (self.n_adapters,), _I32, True))
+        _check(load_library().lora_muon_step(self._h, _ptr(grad), _ptr(momentum), _ptr(master), _ptr(momentum_out),
+                                             _ptr(master_out), _ptr(pool), float(lr), float(beta),
+                                             1 if nesterov else 0, float(weight_decay), float(rms), _ptr(active),
+                                             _stream(stream)), "lora_muon_step")
+
+    def destroy(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            load_library().lora_muon_destroy(self._h)
+            self._h = _vp()
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass

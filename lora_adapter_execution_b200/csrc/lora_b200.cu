@@ -17,6 +17,7 @@
 #include "tsqr.cuh"
 #include "compress.cuh"
 #include "fp8.cuh"
+#include "muon.cuh"
 
 using namespace lora;
 
@@ -1800,3 +1801,6 @@ int lora_switch_apply(lora_switch_t sw, uint16_t *W, const uint16_t *A_pool, con
 
 // The layer over an 8-bit frozen base (and its kernels' launch attributes).
 #include "fp8_api.inc"
+
+// The Muon step of a pool of adapter factors.
+#include "muon_api.inc"
