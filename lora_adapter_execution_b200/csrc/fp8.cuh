@@ -142,33 +142,62 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------ product
-// 12 warps: 0 copies A (and the adapter blocks), 1 issues the MMAs and owns
-// TMEM, 2 copies W, 3 is the fix-up warp of adapter blocks (as in gemm.cuh), and
-// two warpgroups 4..7, 8..11 accumulate: thread = output row (a TMEM lane),
-// warpgroup h = columns [h·BN/2, (h+1)·BN/2) of the tile, so at BN = 256 each
-// warpgroup meets exactly one weight block per K block.
-constexpr int kF8Threads = 384;
+// 12 warps: 0 copies A, W and the adapter blocks, 1 and 2 issue the MMAs (1 owns
+// TMEM), 3 is the fix-up warp of adapter blocks (as in gemm.cuh), and two
+// warpgroups accumulate: thread = output row (a TMEM lane), warpgroup h = columns
+// [h·BN/2, (h+1)·BN/2) of the tile, so at BN = 256 each meets one weight block per
+// K block. Two issuing warps, because two waits, four MMAs and two commits took one
+// about 1,100 cycles a block beside everything else: warp 1 + e takes the stages of
+// parity e and fills TMEM buffers of its own. A tile's adapter blocks therefore end
+// in up to two buffers (those on even stages, those on odd ones), drained before
+// the base blocks'. What bounds it: the loads in flight (4 stages of 48 KB) against
+// their latency, 760 cycles a block where the MMAs take 512, and the hand-over of
+// the buffers. 5003 x 11008 x 4096: 272 us, 1.66 PFLOP/s (one issuing warp, scales
+// loaded a block ahead: 373 us).
+constexpr int kF8Groups = 2;                   // accumulating warpgroups
+constexpr int kF8Sum = 128 * kF8Groups;        // accumulating threads
+constexpr int kF8Threads = 128 + kF8Sum;
 constexpr int kF8K = 128;  // bytes (= elements) of K per stage: one scale block, one swizzle row
 constexpr int kF8StageA = kBM * kF8K;  // 16 KB; an adapter block's s·U image has the same size
 // Registers a thread at BN = 256 after the split: what the copying warps give up
 // covers what the accumulating ones take (the launch's 168 per thread).
 constexpr int kF8RegsCopy = 64, kF8RegsSum = 216;
-static_assert(128 * kF8RegsCopy + 256 * kF8RegsSum <= 168 * kF8Threads, "register split");
+static_assert(128 * kF8RegsCopy + kF8Sum * kF8RegsSum <= 168 * kF8Threads, "register split");
+// K blocks whose scales a thread has on their way (cp.async into slots of its
+// own, so no barrier). Under the operands' load an L2 access takes several
+// thousand cycles: 3 blocks ahead cost a tenth of the time (5003 x 11008 x 4096:
+// 310 us, 278 us with 15 ahead).
+constexpr int kScaleAhead = 16;
 template <int BN>
 struct F8 {
   static constexpr int kStageB = BN * kF8K;
   static constexpr int kStage = kF8StageA + kStageB;
   static constexpr int kStages = BN == 256 ? 4 : 6;
   static constexpr int kBuf = BN == 256 ? 2 : 4;       // TMEM buffers (512 columns in all)
-  static constexpr int kCols = BN / 2;                 // columns per accumulating thread
+  static constexpr int kCols = BN / kF8Groups;                 // columns per accumulating thread
   static constexpr int kSlot = (BN / 64) * 16 * 128;   // one 16-row slice of B_pool over the tile's columns
   static constexpr int kBars = 512;
-  static constexpr int kSmem = 1024 + kStages * kStage + kBars;
+  // scales on their way to the accumulating threads: [kScaleAhead][threads]
+  static constexpr int kScales = kScaleAhead * kF8Sum * 4;
+  static constexpr int kSmem = 1024 + kStages * kStage + kBars + kScales;
 };
+static_assert(F8<128>::kStages % 2 == 0 && F8<256>::kStages % 2 == 0, "a stage belongs to one issuing warp");
 static_assert(kF8StageA == kAugBlockBytes, "an adapter block's image fills the A half of a stage");
 static_assert(F8<128>::kStages * F8<128>::kStage >= kBM * 128 * 4, "split-K exchange must fit the stage ring");
 static_assert(F8<256>::kStages * F8<256>::kStage >= kBM * 256 * 4, "split-K exchange must fit the stage ring");
 
+// A position in a ring of N buffers and its phase.
+template <int N>
+struct F8Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
 struct Fp8Params {
   GemmParams g;     // geometry, plan tables, output and mask (a_sorted: A rows are in the plan's order)
   const float *Sx;  // [K blocks][T]: scale of A's row i (in A's row order) in K block b
@@ -186,10 +215,33 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint6
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// 32 consecutive fp32 columns of this thread's TMEM lane, waited for (one statement,
+// so that nothing that uses them can move before the wait).
+__device__ __forceinline__ void tmem_ld32w(uint32_t taddr, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
 // Instruction descriptor, kind::f8f6f4 with e4m3 A/B (format 0) and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// 4 bytes from global to this thread's shared slot, or zero when bytes is 0.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
@@ -197,6 +249,14 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
 // Every thread of the CTA meets here once, from either branch of the kernel.
 __device__ __forceinline__ void f8_join() { asm volatile("barrier.sync 0, %0;" ::"n"(kF8Threads) : "memory"); }
 
@@ -240,7 +300,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
     for (int b = 0; b < C::kBuf; ++b) {
       mbar_init(accf0 + 8 * b, 1);
-      mbar_init(acce0 + 8 * b, 8);  // one arrival per accumulating warp
+      mbar_init(acce0 + 8 * b, kF8Sum / 32);  // one arrival per accumulating warp
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -267,9 +327,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (warp < 4) {
     if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RegsCopy));
     if (warp == 0) {
-      // ------------------------------------------------ A rows and adapter blocks
+      // ------------------------------------------------ copies: A, W, adapter blocks
       if (lane == 0) {
         prefetch_tmap(&mapA);
+        prefetch_tmap(&mapB);
         int stage = 0;
         uint32_t phase = 0;
         int tile;
@@ -287,9 +348,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             const uint32_t b_dst = a_dst + kF8StageA;
             const uint32_t fb = full0 + 8 * stage;
             if (blk < KB) {
-              // the expected bytes cover the W copy of warp 2 too
               mbar_arrive_expect_tx(fb, C::kStage);
               tma_load_2d(a_dst, &mapA, fb, blk * kF8K, td.row0);
+              if (B_KMAJOR) {
+                tma_load_2d(b_dst, &mapB, fb, blk * kF8K, n0);
+              } else {
+                for (int j = 0; j < BN / 128; ++j)
+                  tma_load_2d(b_dst + j * 16384, &mapB, fb, n0 + j * 128, blk * kF8K);
+              }
             } else {
               const AugBlockDesc *ab = p.augblocks + td.aug0 + (blk - KB);
               const int4 prow = __ldg(reinterpret_cast<const int4 *>(ab));
@@ -310,37 +376,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                       tma_load_2d(b_dst + u * C::kSlot + j * 2048, &mapBl, fb, n0 + j * 64, prow_s[u]);
                   }
                 }
-              }
-            }
-            if (++stage == C::kStages) { stage = 0; phase ^= 1; }
-          }
-        }
-      }
-    } else if (warp == 2) {
-      // ------------------------------------------------ W (the B half of base stages)
-      if (lane == 0) {
-        prefetch_tmap(&mapB);
-        int stage = 0;
-        uint32_t phase = 0;
-        int tile;
-        for (int k = 0; !*abort_flag && cta_tile(p, k, tile0, tile_step, n_tiles, tile); ++k) {
-          int mt, nt;
-          tile_coords(tile, p, mt, nt);
-          const int kaug = has_plan ? p.tiles[mt].kaug : 0;
-          const int n0 = nt * BN;
-          const BlockRange br = block_range(KB, (kaug + kAugBlock - 1) / kAugBlock, q, S);
-          const int nblk = br.count();
-          for (int i = 0; i < nblk; ++i) {
-            const int blk = br.block(i, KB);
-            if (!mbar_wait(empty0 + 8 * stage, phase ^ 1)) { *abort_flag = 1; break; }
-            if (blk < KB) {
-              const uint32_t b_dst = stage0 + stage * C::kStage + kF8StageA;
-              const uint32_t fb = full0 + 8 * stage;
-              if (B_KMAJOR) {
-                tma_load_2d(b_dst, &mapB, fb, blk * kF8K, n0);
-              } else {
-                for (int j = 0; j < BN / 128; ++j)
-                  tma_load_2d(b_dst + j * 16384, &mapB, fb, n0 + j * 128, blk * kF8K);
               }
             }
             if (++stage == C::kStages) { stage = 0; phase ^= 1; }
@@ -395,8 +430,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           if (!ok) break;
         }
       }
-    } else if (lane == 0) {
-      // ------------------------------------------------ MMA issuer (warp 1)
+    } else {
+      // ------------------------------------------------ MMA issuers (the whole warp
+      // runs the loop, one elected lane issues, so descriptors stay in uniform registers)
       constexpr uint32_t kIdesc = idesc_e4m3(kBM, BN, false, !B_KMAJOR);
       constexpr uint32_t kIdescAug = idesc_bf16(kBM, BN, false, true);
       // A K-major, 128-byte rows: 8-row groups 1 KB apart, a K = 32 step 32 bytes on.
@@ -407,10 +443,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       constexpr uint64_t kAStep = 32 >> 4;
       constexpr uint64_t kBStep = B_KMAJOR ? (32 >> 4) : (4096 >> 4);
       const uint32_t ready0 = has_plan ? fixed0 : full0;
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
+      const int e = warp - 1;
+      F8Ring<C::kBuf / 2> ring;
+      int stage = 0;
+      uint32_t phase = 0;
       int tile;
-      for (int k = 0; !*abort_flag && cta_tile(p, k, tile0, tile_step, n_tiles, tile); ++k) {
+      for (int k = 0;; ++k) {
+        const bool go = !*abort_flag && cta_tile(p, k, tile0, tile_step, n_tiles, tile);
+        if (!__shfl_sync(0xFFFFFFFFu, go ? 1 : 0, 0)) break;
         int mt, nt;
         tile_coords(tile, p, mt, nt);
         const int kaug = has_plan ? p.tiles[mt].kaug : 0;
@@ -418,37 +458,45 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         const int nblk = br.count(), naug = br.naug();
         bool ok = true;
         for (int i = 0; i < nblk; ++i) {
-          const int blk = br.block(i, KB);
-          // the adapter blocks share one buffer, each base block has its own
-          const bool first = i == 0 || i >= naug;
-          if (first) {
-            if (!mbar_wait(acce0 + 8 * buf, bphase ^ 1)) { *abort_flag = 1; ok = false; break; }
+          if ((stage & 1) != e) {  // the other warp's
+            if (++stage == C::kStages) { stage = 0; phase ^= 1; }
+            continue;
           }
-          if (!mbar_wait(ready0 + 8 * stage, phase)) { *abort_flag = 1; ok = false; break; }
+          const int blk = br.block(i, KB);
+          // this warp's adapter blocks of a tile share one buffer, each base block has its own
+          const bool first = i < 2 || i >= naug, last = i + 2 >= naug;
+          const int buf = e + 2 * ring.slot;
+          if ((first && !__all_sync(0xFFFFFFFFu, mbar_wait(acce0 + 8 * buf, ring.phase ^ 1))) ||
+              !__all_sync(0xFFFFFFFFu, mbar_wait(ready0 + 8 * stage, phase))) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + buf * BN;
           const uint64_t ad = adesc0 + static_cast<uint64_t>(stage * (C::kStage >> 4));
-          if (blk < KB) {
-            const uint64_t bd = bdesc0 + static_cast<uint64_t>(stage * (C::kStage >> 4));
-            umma_e4m3(d_tmem, ad, bd, kIdesc, 0u);
-            umma_e4m3(d_tmem, ad + kAStep, bd + kBStep, kIdesc, 1u);
-            umma_e4m3(d_tmem, ad + 2 * kAStep, bd + 2 * kBStep, kIdesc, 1u);
-            umma_e4m3(d_tmem, ad + 3 * kAStep, bd + 3 * kBStep, kIdesc, 1u);
-          } else {
-            // bf16 image columns against the slots of B_pool rows, 16 ranks a step
-            const int steps = min(4, (kaug - (blk - KB) * kAugBlock) / 16);
-            const uint32_t map = bmap[stage];
-            const uint32_t b_s = stage0 + stage * C::kStage + kF8StageA;
-            for (int u = 0; u < steps; ++u) {
-              const uint64_t bd = sdesc_sw128(b_s + ((map >> (2 * u)) & 3u) * C::kSlot, 2048, 1024);
-              umma_bf16(d_tmem, ad + u * kAStep, bd, kIdescAug, (first && u == 0) ? 0u : 1u);
+          if (elect_one()) {
+            if (blk < KB) {
+              const uint64_t bd = bdesc0 + static_cast<uint64_t>(stage * (C::kStage >> 4));
+              umma_e4m3(d_tmem, ad, bd, kIdesc, 0u);
+              umma_e4m3(d_tmem, ad + kAStep, bd + kBStep, kIdesc, 1u);
+              umma_e4m3(d_tmem, ad + 2 * kAStep, bd + 2 * kBStep, kIdesc, 1u);
+              umma_e4m3(d_tmem, ad + 3 * kAStep, bd + 3 * kBStep, kIdesc, 1u);
+            } else {
+              // bf16 image columns against the slots of B_pool rows, 16 ranks a step
+              const int steps = min(4, (kaug - (blk - KB) * kAugBlock) / 16);
+              const uint32_t map = bmap[stage];
+              const uint32_t b_s = stage0 + stage * C::kStage + kF8StageA;
+              for (int u = 0; u < steps; ++u) {
+                const uint64_t bd = sdesc_sw128(b_s + ((map >> (2 * u)) & 3u) * C::kSlot, 2048, 1024);
+                umma_bf16(d_tmem, ad + u * kAStep, bd, kIdescAug, (i < 2 && u == 0) ? 0u : 1u);
+              }
             }
+            umma_commit(empty0 + 8 * stage);
+            if (last) umma_commit(accf0 + 8 * buf);  // the buffer is complete
           }
-          umma_commit(empty0 + 8 * stage);
-          if (i >= naug - 1) {  // the buffer is complete
-            umma_commit(accf0 + 8 * buf);
-            if (++buf == C::kBuf) { buf = 0; bphase ^= 1; }
-          }
+          __syncwarp();
+          if (last) ring.next();
           if (++stage == C::kStages) { stage = 0; phase ^= 1; }
         }
         if (!ok) break;
@@ -471,8 +519,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + h * C::kCols;
-    int buf = 0;
-    uint32_t bphase = 0;
+    uint32_t rings = 0;  // buffers of even and of odd stages drained so far, a byte each
+    int par = 0;                       // parity of the next block's stage
     int tile;
     for (int k = 0; !*abort_flag && cta_tile(p, k, tile0, tile_step, n_tiles, tile); ++k) {
       int mt, nt;
@@ -483,54 +531,88 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       const int col0 = nt * BN + h * C::kCols;
       int64_t orig = 0;
       if (valid) orig = has_plan ? (td.contig >= 0 ? td.contig + row : p.perm[td.row0 + row]) : td.row0 + row;
-      // scales of K block b for this row and these columns
-      const int nb = col0 / kQBlock;
-      const float *sx = fp.Sx + td.row0 + row;
-      const float *sw = fp.Sw + static_cast<int64_t>(nb) * fp.sw_n;
-      auto scale_of = [&](int b) -> float {
-        if (!valid || nb >= fp.n_nb) return 0.f;
-        return __ldg(sx + static_cast<int64_t>(b) * p.T) * __ldg(sw + static_cast<int64_t>(b) * fp.sw_k);
-      };
       float acc[C::kCols];
 #pragma unroll
       for (int i = 0; i < C::kCols; ++i) acc[i] = 0.f;
-      const int ngroups = br.nbase + (br.naug() > 0 ? 1 : 0);
-      const int first_base = ngroups - br.nbase;
-      float s_next = br.nbase > 0 ? scale_of(br.kb_lo) : 0.f;
-      bool ok = true;
-      for (int g = 0; g < ngroups; ++g) {
-        float s = 1.f;
-        if (g >= first_base) {
-          s = s_next;
-          if (g + 1 < ngroups) s_next = scale_of(br.kb_lo + g - first_base + 1);
-        }
-        if (!mbar_wait(accf0 + 8 * buf, bphase)) { *abort_flag = 1; ok = false; break; }
-        tc_fence_after();
-        // (a warp without rows has nothing to add)
+      // Scales: the row's by cp.async into slots of the thread's own (no barrier),
+      // kScaleAhead - 1 K blocks ahead; the weight block's, the same for the warp,
+      // 32 K blocks at a time in the lanes of one register.
+      const int nb = col0 / kQBlock;
+      const bool in = valid && nb < fp.n_nb;
+      const uint32_t sc = smem_u32(smem + C::kStages * C::kStage + C::kBars) + (threadIdx.x - 128) * 4;
+      const uint32_t sc_bytes = in ? 4u : 0u;  // 0: the slot becomes zero
+      const float *sx = in ? fp.Sx + static_cast<int64_t>(br.kb_lo) * p.T + td.row0 + row : fp.Sx;
+      const int64_t sx_step = in ? p.T : 0;
+      const float *sw = fp.Sw + static_cast<int64_t>(min(nb, fp.n_nb - 1)) * fp.sw_n + static_cast<int64_t>(br.kb_lo) * fp.sw_k;
+      auto fetch_scale = [&](int j, int slot) {
+        if (j < br.nbase) cp_async4(sc + slot * (kF8Sum * 4), sx, sc_bytes);
+        cp_async_commit();
+        sx += sx_step;
+      };
 #pragma unroll
-        for (int c = 0; c < C::kCols / 32; ++c) {
-          if (quarter * 32 >= td.rows) break;
-          uint32_t v[32];
-          tmem_ld32(lane_base + buf * BN + c * 32, v);
-          tmem_wait_ld();
-          if (DROP && g < first_base) {
+      for (int j = 0; j < kScaleAhead - 1; ++j) fetch_scale(j, j);
+      bool ok = true;
+      // one complete TMEM buffer of the stages of parity e: each 16 columns handed
+      // to `add` as they arrive, the buffer released once all are in registers
+      auto drain = [&](int e, auto add) -> bool {
+        const uint32_t n = (rings >> (8 * e)) & 0xFFu;
+        const int buf = e + 2 * (n % (C::kBuf / 2));
+        if (!mbar_wait(accf0 + 8 * buf, (n / (C::kBuf / 2)) & 1u)) { *abort_flag = 1; return false; }
+        tc_fence_after();
+        const uint32_t ta = lane_base + buf * BN;
+        if (quarter * 32 < td.rows) {  // (a warp without rows has nothing to add)
+#pragma unroll
+          for (int c = 0; c < C::kCols / 32; ++c) {
+            float v[32];
+            tmem_ld32w(ta + c * 32, v);
+            if (c + 1 == C::kCols / 32) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(acce0 + 8 * buf);
+            }
+            add(c, v);
+          }
+        } else if (lane == 0) {
+          mbar_arrive(acce0 + 8 * buf);
+        }
+        // (the count of parity e, modulo a power of two that its byte holds)
+        rings = (rings & ~(0xFFu << (8 * e))) | (((n + 1) & 0x7Fu) << (8 * e));
+        return true;
+      };
+      // the adapter term first, as it is or masked: the blocks on this parity's
+      // stages, then those on the other's
+      const float one = DROP ? p.inv_keep : 1.f;
+      const int naug = br.naug();
+#pragma unroll 1
+      for (int u = 0; ok && u < min(naug, 2); ++u) {
+        ok = drain(par ^ u, [&](int c, const float (&v)[32]) {
+          if constexpr (DROP) {
             const int cc = col0 + c * 32;
             uint32_t keep = 0;
             if (valid && cc < p.N)
               keep = p.keep_bits ? __ldg(p.keep_bits + orig * p.wpr + (cc >> 5))
                                  : keep_mask32(p.seed, p.thr, static_cast<uint64_t>(orig * p.N + cc));
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              acc[c * 32 + i] = ((keep >> i) & 1u) ? p.inv_keep * __uint_as_float(v[i]) : 0.f;
+            for (int i = 0; i < 32; ++i) acc[c * 32 + i] += ((keep >> i) & 1u) ? one * v[i] : 0.f;
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(s, __uint_as_float(v[i]), acc[c * 32 + i]);
+            for (int i = 0; i < 32; ++i) acc[c * 32 + i] += v[i];
           }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acce0 + 8 * buf);
-        if (++buf == C::kBuf) { buf = 0; bphase ^= 1; }
+        });
+      }
+      par ^= naug & 1;
+      float sw_lane = 0.f;
+#pragma unroll 1
+      for (int j = 0; ok && j < br.nbase; ++j) {
+        if ((j & 31) == 0) sw_lane = j + lane < br.nbase ? __ldg(sw + static_cast<int64_t>(j + lane) * fp.sw_k) : 0.f;
+        cp_async_wait<kScaleAhead - 2>();
+        const float s = ld_shared_f32(sc + (j % kScaleAhead) * (kF8Sum * 4)) * __shfl_sync(0xFFFFFFFFu, sw_lane, j & 31);
+        fetch_scale(j + kScaleAhead - 1, (j + kScaleAhead - 1) % kScaleAhead);
+        ok = drain(par, [&](int c, const float (&v)[32]) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(s, v[i], acc[c * 32 + i]);
+        });
+        par ^= 1;
       }
       if (!ok) break;
       if (S == 1) {
@@ -539,12 +621,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
           for (int j = 0; j < C::kCols / 8; ++j) {
             if (col0 + 8 * j < p.N) {
-              uint4 o;
-              o.x = pack_bf16x2(acc[8 * j + 0], acc[8 * j + 1]);
-              o.y = pack_bf16x2(acc[8 * j + 2], acc[8 * j + 3]);
-              o.z = pack_bf16x2(acc[8 * j + 4], acc[8 * j + 5]);
-              o.w = pack_bf16x2(acc[8 * j + 6], acc[8 * j + 7]);
-              dst[j] = o;
+              const float *a = acc + 8 * j;
+              dst[j] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                                  pack_bf16x2(a[6], a[7]));
             }
           }
         }
