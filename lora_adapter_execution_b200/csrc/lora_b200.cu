@@ -39,6 +39,7 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 bool qr_kernel_attributes();   // qr_api.inc
 bool fp8_kernel_attributes();  // fp8_api.inc
+bool muon_kernel_attributes();  // muon_api.inc
 
 int device_state(DeviceState **out) {
   int dev = 0;
@@ -87,6 +88,7 @@ int device_state(DeviceState **out) {
                                      tc_smem(kTcMaxR)) == cudaSuccess;
           ok &= qr_kernel_attributes();
           ok &= fp8_kernel_attributes();
+          ok &= muon_kernel_attributes();
           if (!ok) d.status = LORA_ERR_CUDA;
           for (int S = 1; ok && S <= 4; S *= 2) {
             cudaLaunchConfig_t cfg{};

@@ -18,6 +18,8 @@
 #pragma once
 
 #include "common.cuh"
+#include "fp8.cuh"   // ld_cluster_f32
+#include "gemm.cuh"  // cluster_barrier, map_rank
 
 namespace lora {
 
@@ -67,6 +69,12 @@ __device__ __forceinline__ void dmma(double (&d)[4], double a0, double a1, doubl
       "mma.sync.aligned.m16n8k4.row.col.f64.f64.f64.f64 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
       : "+d"(d[0]), "+d"(d[1]), "+d"(d[2]), "+d"(d[3])
       : "d"(a0), "d"(a1), "d"(b));
+}
+
+__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // ------------------------------------------------------------------ momentum
@@ -331,6 +339,324 @@ __global__ void __launch_bounds__(256)
         muon_store4(out, (ad.row0 + row) * d + c0 + tc, step, make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]));
     }
   }
+}
+
+// ------------------------------------------------------------------ one launch per step
+// Ranks up to 64 whose rows fit in shared memory: a cluster of CTAs per adapter,
+// each CTA one slice of the columns, kept on chip from the first read to the
+// result, so the rows cross HBM once (22 bytes an element for a step, 8 for an
+// orthogonalisation). CTA: momentum and U of its slice (fp32, in shared memory),
+// its slice's Gram matrix; the cluster's first CTA adds the slices' (through
+// distributed shared memory, in order) and iterates; every CTA takes P from it and
+// forms its slice of the result.
+//
+// Shared memory: U [RP][slice] fp32, column c of row i at c ^ ((i & 7) << 2)
+// (a fragment's eight rows of four columns then lie in 32 different banks); three
+// RP x RP matrices of doubles, column c of row i at c ^ ((i & 3) << 2) likewise.
+// The space of the matrices first holds the warps' partial Gram matrices.
+template <int RP>
+struct MuF {
+  static constexpr int M = RP / 16;
+  static constexpr int kTiles = M * (M + 1);         // 16 x 8 tiles on or above the diagonal blocks
+  static constexpr int kGroups = M == 1 ? 1 : M == 2 ? 2 : 4;  // warps that share a k range, by tiles
+  static constexpr int kSplits = 8 / kGroups;        // k ranges
+  static constexpr int kPer = (kTiles + kGroups - 1) / kGroups;  // tiles per warp, Gram
+  static constexpr int kPerP = (kTiles + 7) / 8;     // tiles per warp, products
+  static constexpr int kMat = RP * RP;               // doubles
+  static constexpr int kMatBytes = (kSplits > 3 ? kSplits : 3) * kMat * 8;
+  static constexpr int kRows = RP <= 32 ? 4 : 8;     // rows per thread of the application
+  static constexpr int kCtas = RP == 16 ? 4 : RP == 32 ? 2 : 1;  // CTAs an SM should hold
+};
+// tile t of the upper list: row block i, column tile j (of 8), j = 2i .. 2M - 1
+template <int M>
+__device__ __forceinline__ void mu_tile(int t, int &i, int &j) {
+  i = 0;
+#pragma unroll
+  for (int k = 0; k < M - 1; ++k)
+    if (i == k && t >= 2 * (M - k)) {
+      t -= 2 * (M - k);
+      i = k + 1;
+    }
+  j = 2 * i + t;
+}
+template <int RP>
+__device__ __forceinline__ int mu_at(int row, int col) { return row * RP + (col ^ ((row & 3) << 2)); }
+
+struct MuonFused {
+  const float *g, *m;   // gradient and momentum in (m null: U = g)
+  float *m_out;
+  float beta, omb;
+  int nesterov;
+  int64_t d;
+  int slice;            // columns per CTA, a multiple of 32
+};
+
+// this warp's tiles of A·B (symmetric commuting operands) in registers
+template <int RP>
+__device__ __forceinline__ void mu_product(const double *A, const double *B, int warp, int lane,
+                                           double (&acc)[MuF<RP>::kPerP][4]) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int q = 0; q < MuF<RP>::kPerP; ++q) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[q][e] = 0.0;
+    const int tile = warp + 8 * q;
+    if (tile < MuF<RP>::kTiles) {
+      int i, j;
+      mu_tile<MuF<RP>::M>(tile, i, j);
+      const double *a0 = A + (16 * i + g) * RP, *a1 = a0 + 8 * RP, *b = B + (8 * j + g) * RP;
+      const int sw = (g & 3) << 2;
+#pragma unroll
+      for (int k = 0; k < RP; k += 4) {
+        const int o = (k ^ sw) + t;
+        dmma(acc[q], a0[o], a1[o], b[o]);
+      }
+    }
+  }
+}
+// ... and to shared memory, with their mirrors; poly: c·acc + b·A + a·I instead
+template <int RP>
+__device__ __forceinline__ void mu_write(double *C, const double *A, bool poly, int rank, int warp, int lane,
+                                         const double (&acc)[MuF<RP>::kPerP][4]) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int q = 0; q < MuF<RP>::kPerP; ++q) {
+    const int tile = warp + 8 * q;
+    if (tile < MuF<RP>::kTiles) {
+      int i, j;
+      mu_tile<MuF<RP>::M>(tile, i, j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 16 * i + g + (e >> 1) * 8, col = 8 * j + 2 * t + (e & 1);
+        double v = acc[q][e];
+        if (poly) v = kNsCd * v + kNsBd * A[mu_at<RP>(row, col)] + (row == col && row < rank ? kNsAd : 0.0);
+        C[mu_at<RP>(row, col)] = v;
+        if ((j >> 1) != i) C[mu_at<RP>(col, row)] = v;
+      }
+    }
+  }
+}
+
+template <int RP>
+__global__ void __launch_bounds__(256, MuF<RP>::kCtas)
+    lora_muon_fused_kernel(const MuonAdapter *__restrict__ ads, const int32_t *__restrict__ active, MuonFused p,
+                           MuonOutput out) {
+  using F = MuF<RP>;
+  extern __shared__ __align__(1024) uint8_t mu_smem[];
+  double *mat = reinterpret_cast<double *>(mu_smem);
+  float *us = reinterpret_cast<float *>(mu_smem + F::kMatBytes);
+  uint32_t ncta, rank_in;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncta));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank_in));
+  const MuonAdapter ad = ads[blockIdx.x / ncta];
+  if (active && active[ad.index] == 0) return;  // the whole cluster
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = ad.rank;
+  const int64_t c0 = static_cast<int64_t>(rank_in) * p.slice;
+  const int nc4 = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(p.slice), p.d - c0)) / 4);
+  const int64_t base = ad.row0 * p.d + c0;
+
+  // ---- the slice's rows: momentum, U
+  {
+    constexpr int kUn = 4;
+    const int total = r * nc4;
+    int row = 0, c = static_cast<int>(threadIdx.x);
+    if (nc4 > 0) {
+      row = c / nc4;
+      c -= row * nc4;
+    }
+    for (int e0 = threadIdx.x; e0 < total; e0 += 256 * kUn) {
+      float4 gv[kUn], mv[kUn];
+      int rr[kUn], cc[kUn];
+#pragma unroll
+      for (int u = 0; u < kUn; ++u) {
+        rr[u] = row;
+        cc[u] = c;
+        if (e0 + 256 * u < total) {
+          const int64_t o = base + row * p.d + 4 * c;
+          gv[u] = *reinterpret_cast<const float4 *>(p.g + o);
+          if (p.m) mv[u] = *reinterpret_cast<const float4 *>(p.m + o);
+        }
+        c += 256;
+        while (c >= nc4) {
+          c -= nc4;
+          ++row;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUn; ++u) {
+        if (e0 + 256 * u < total) {
+          float4 v = gv[u];
+          if (p.m) {
+            float4 m = mv[u];
+            m.x = fmaf(p.beta, m.x, p.omb * v.x);
+            m.y = fmaf(p.beta, m.y, p.omb * v.y);
+            m.z = fmaf(p.beta, m.z, p.omb * v.z);
+            m.w = fmaf(p.beta, m.w, p.omb * v.w);
+            *reinterpret_cast<float4 *>(p.m_out + base + rr[u] * p.d + 4 * cc[u]) = m;
+            if (p.nesterov) {
+              v.x = fmaf(p.beta, m.x, p.omb * v.x);
+              v.y = fmaf(p.beta, m.y, p.omb * v.y);
+              v.z = fmaf(p.beta, m.z, p.omb * v.z);
+              v.w = fmaf(p.beta, m.w, p.omb * v.w);
+            } else {
+              v = m;
+            }
+          }
+          *reinterpret_cast<float4 *>(us + rr[u] * p.slice + ((4 * cc[u]) ^ ((rr[u] & 7) << 2))) = v;
+        }
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- the slice's Gram matrix: warp = (k range, tiles); lane (g, t) needs the same
+  // values U[16 i + g (+ 8)][k + t] as A fragments and as B fragments
+  {
+    const int grp = warp % F::kGroups, ks = warp / F::kGroups;
+    const int g = lane >> 2, t = lane & 3;
+    double acc[F::kPer][4] = {};
+    for (int kk = ks; kk < nc4; kk += F::kSplits) {
+      double v[2 * F::M];
+#pragma unroll
+      for (int b = 0; b < 2 * F::M; ++b)
+        v[b] = 8 * b + g < r ? static_cast<double>(us[(8 * b + g) * p.slice + ((4 * kk) ^ (g << 2)) + t]) : 0.0;
+#pragma unroll
+      for (int q = 0; q < F::kPer; ++q) {
+        const int tile = grp + F::kGroups * q;
+        if (F::kGroups == 1) {
+          dmma(acc[q], v[0], v[1], v[q]);  // RP = 16: tiles (0, 0), (0, 1)
+        } else if (tile < F::kTiles) {
+          int i, j;
+          mu_tile<F::M>(tile, i, j);
+          double a0 = 0.0, a1 = 0.0, bb = 0.0;
+#pragma unroll
+          for (int b = 0; b < 2 * F::M; ++b) {  // (i, j differ per warp: select, no indexing)
+            if (b == 2 * i) a0 = v[b];
+            if (b == 2 * i + 1) a1 = v[b];
+            if (b == j) bb = v[b];
+          }
+          dmma(acc[q], a0, a1, bb);
+        }
+      }
+    }
+    double *red = mat + ks * F::kMat;
+#pragma unroll
+    for (int q = 0; q < F::kPer; ++q) {
+      const int tile = grp + F::kGroups * q;
+      if (tile < F::kTiles) {
+        int i, j;
+        mu_tile<F::M>(tile, i, j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          red[mu_at<RP>(16 * i + g + (e >> 1) * 8, 8 * j + 2 * t + (e & 1))] = acc[q][e];
+      }
+    }
+  }
+  __syncthreads();
+  // the k ranges' sums, in order (only the blocks on and above the diagonal were formed)
+  for (int e = threadIdx.x; e < F::kMat; e += 256) {
+    const int row = e / RP, col = e % RP;
+    if ((col >> 4) >= (row >> 4)) {
+      const int o = mu_at<RP>(row, col);
+      double v = mat[o];
+      for (int k = 1; k < F::kSplits; ++k) v += mat[k * F::kMat + o];
+      mat[o] = v;
+    }
+  }
+  if (ncta > 1) cluster_barrier();
+  else __syncthreads();
+  float *pf = reinterpret_cast<float *>(mat + F::kMat);  // P as fp32 [RP][RP], in the second matrix's place
+  if (rank_in == 0) {
+    // ---- the first CTA: G0, the iteration, P
+    double *G = mat, *Q = mat + F::kMat, *P = mat + 2 * F::kMat;
+    for (int e = threadIdx.x; e < F::kMat; e += 256) {
+      const int row = e / RP, col = e % RP;
+      if ((col >> 4) >= (row >> 4)) {
+        const int o = mu_at<RP>(row, col);
+        double v = G[o];
+        for (uint32_t q = 1; q < ncta; ++q) v += ld_cluster_f64(map_rank(smem_u32(G + o), q));
+        G[o] = v;
+        if ((col >> 4) > (row >> 4)) G[mu_at<RP>(col, row)] = v;
+      }
+    }
+    __syncthreads();
+    double tr = 0.0;
+    for (int i = lane; i < r; i += 32) tr += G[mu_at<RP>(i, i)];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tr += __shfl_xor_sync(0xFFFFFFFFu, tr, o);
+    const double inv = 1.0 / (sqrt(tr) + kNsEps);
+    __syncthreads();
+    for (int e = threadIdx.x; e < F::kMat; e += 256) G[e] *= inv * inv;
+    __syncthreads();
+    double a1[F::kPerP][4], a2[F::kPerP][4];
+#pragma unroll 1
+    for (int step = 0; step < kNsSteps; ++step) {
+      const bool last = step == kNsSteps - 1;
+      mu_product<RP>(G, G, warp, lane, a1);
+      mu_write<RP>(Q, G, true, r, warp, lane, a1);  // Q's last readers are behind a barrier
+      if (step == 0) mu_write<RP>(P, G, true, r, warp, lane, a1);  // the first Q is P
+      __syncthreads();
+      if (!last) mu_product<RP>(Q, G, warp, lane, a1);
+      if (step > 0) mu_product<RP>(P, Q, warp, lane, a2);
+      __syncthreads();  // every read of G and P is done: their products replace them
+      if (!last) mu_write<RP>(G, nullptr, false, r, warp, lane, a1);
+      if (step > 0) mu_write<RP>(P, nullptr, false, r, warp, lane, a2);
+      __syncthreads();
+      if (!last) {
+        mu_product<RP>(Q, G, warp, lane, a1);  // Q·(Q·G)
+        __syncthreads();
+        mu_write<RP>(G, nullptr, false, r, warp, lane, a1);
+        __syncthreads();
+      }
+    }
+    for (int e = threadIdx.x; e < F::kMat; e += 256) pf[e] = static_cast<float>(P[mu_at<RP>(e / RP, e % RP)] * inv);
+  }
+  if (ncta > 1) {
+    cluster_barrier();
+    if (rank_in != 0) {
+      const uint32_t src = map_rank(smem_u32(pf), 0);
+      for (int e = threadIdx.x; e < F::kMat; e += 256) pf[e] = ld_cluster_f32(src + 4 * e);
+    }
+    // the first CTA stays until all have read P
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  __syncthreads();
+
+  // ---- O = P·U of the slice: kRows rows x 4 columns per thread (P is symmetric: row k
+  // holds column k)
+  const float step = muon_step_size(out, r, p.d);
+  const int ngrp = (r + F::kRows - 1) / F::kRows;
+  for (int e = threadIdx.x; e < ngrp * nc4; e += 256) {
+    const int grp = e / nc4, c = 4 * (e - grp * nc4);
+    float4 acc[F::kRows];
+#pragma unroll
+    for (int i = 0; i < F::kRows; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < r; ++k) {
+      const float4 u = *reinterpret_cast<const float4 *>(us + k * p.slice + (c ^ ((k & 7) << 2)));
+      const float4 *pk = reinterpret_cast<const float4 *>(pf + k * RP + grp * F::kRows);
+#pragma unroll
+      for (int i4 = 0; i4 < F::kRows / 4; ++i4) {
+        const float4 a = pk[i4];
+        const float av[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float4 &o = acc[4 * i4 + i];
+          o.x = fmaf(av[i], u.x, o.x);
+          o.y = fmaf(av[i], u.y, o.y);
+          o.z = fmaf(av[i], u.z, o.z);
+          o.w = fmaf(av[i], u.w, o.w);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < F::kRows; ++i) {
+      const int row = grp * F::kRows + i;
+      if (row < r) muon_store4(out, base + row * p.d + c, step, acc[i]);
+    }
+  }
+  __syncwarp();
+  if (ncta > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace lora
