@@ -268,12 +268,7 @@ struct MuonOutput {
   float keep;           // 1 - lr·wd
   float lr, rms;        // update w by -lr·gain·O, gain = rms·sqrt(max(rank, d)) (rms > 0) or 1
 };
-__device__ __forceinline__ void muon_store4(const MuonOutput &o, int64_t ofs, float step, float4 v) {
-  if (o.O) {
-    *reinterpret_cast<float4 *>(o.O + ofs) = v;
-    return;
-  }
-  const float4 w = *reinterpret_cast<const float4 *>(o.w + ofs);
+__device__ __forceinline__ void muon_store4(const MuonOutput &o, int64_t ofs, float step, float4 v, float4 w) {
   float4 n;
   n.x = fmaf(o.keep, w.x, -step * v.x);
   n.y = fmaf(o.keep, w.y, -step * v.y);
@@ -282,6 +277,10 @@ __device__ __forceinline__ void muon_store4(const MuonOutput &o, int64_t ofs, fl
   *reinterpret_cast<float4 *>(o.w_out + ofs) = n;
   if (o.pool)
     *reinterpret_cast<uint2 *>(o.pool + ofs) = make_uint2(pack_bf16x2(n.x, n.y), pack_bf16x2(n.z, n.w));
+}
+__device__ __forceinline__ void muon_store4(const MuonOutput &o, int64_t ofs, float step, float4 v) {
+  if (o.O) *reinterpret_cast<float4 *>(o.O + ofs) = v;
+  else muon_store4(o, ofs, step, v, *reinterpret_cast<const float4 *>(o.w + ofs));
 }
 __device__ __forceinline__ float muon_step_size(const MuonOutput &o, int rank, int64_t d) {
   const float big = static_cast<float>(rank > d ? rank : d);
@@ -350,37 +349,44 @@ __global__ void __launch_bounds__(256)
 // distributed shared memory, in order) and iterates; every CTA takes P from it and
 // forms its slice of the result.
 //
-// Shared memory: U [RP][slice] fp32, column c of row i at c ^ ((i & 7) << 2)
-// (a fragment's eight rows of four columns then lie in 32 different banks); three
-// RP x RP matrices of doubles, column c of row i at c ^ ((i & 3) << 2) likewise.
-// The space of the matrices first holds the warps' partial Gram matrices.
-template <int RP>
+// Ranks are padded to a multiple of eight, R = 8·NB. The fp64 MMAs work on tiles of 16
+// rows x 8 columns; of a symmetric matrix only those on or above the diagonal's 16 x 16
+// blocks are formed and stored.
+// Shared memory: U [8·NB][slice] fp32, column c of row i at c ^ ((i & 7) << 2) (a
+// fragment's eight rows of four columns then lie in 32 different banks); three
+// matrices of doubles, pitch RP = 8·NB rounded up to 16, column c of row i at
+// c ^ ((i & 3) << 2) likewise. The space of the matrices first holds the warps'
+// partial Gram matrices, as tiles in fragment order.
+template <int NB>
 struct MuF {
-  static constexpr int M = RP / 16;
-  static constexpr int kTiles = M * (M + 1);         // 16 x 8 tiles on or above the diagonal blocks
-  static constexpr int kGroups = M == 1 ? 1 : M == 2 ? 2 : 4;  // warps that share a k range, by tiles
-  static constexpr int kSplits = 8 / kGroups;        // k ranges
-  static constexpr int kPer = (kTiles + kGroups - 1) / kGroups;  // tiles per warp, Gram
-  static constexpr int kPerP = (kTiles + 7) / 8;     // tiles per warp, products
-  static constexpr int kMat = RP * RP;               // doubles
-  static constexpr int kMatBytes = (kSplits > 3 ? kSplits : 3) * kMat * 8;
-  static constexpr int kRows = RP <= 32 ? 4 : 8;     // rows per thread of the application
-  static constexpr int kCtas = RP == 16 ? 4 : RP == 32 ? 2 : 1;  // CTAs an SM should hold
+  static constexpr int M = (NB + 1) / 2;               // 16-row blocks
+  static constexpr int RP = 16 * M;                    // pitch of the matrices
+  static constexpr int R = 8 * NB;                     // padded rank
+  static constexpr int kTiles = NB % 2 ? M * M : M * (M + 1);
+  static constexpr int kPerP = (kTiles + 7) / 8;       // tiles per warp, one product
+  static constexpr int kPerP2 = (2 * kTiles + 7) / 8;  // tiles per warp, two products
+  static constexpr int kMat = RP * RP;                 // doubles
+  static constexpr int kPart = kTiles * 128;           // doubles of a partial Gram matrix
+  static constexpr int kBufs = NB <= 5 ? 8 : 4;        // partial Gram matrices at a time
+  static constexpr int kMatBytes = (kBufs * kPart > 3 * kMat ? kBufs * kPart : 3 * kMat) * 8;
+  static constexpr int kRows = NB <= 4 ? 8 : 16;       // rows per thread of the application
+  static constexpr int kUn = NB == 1 ? 4 : 8;          // 16-byte loads in flight per thread and array
+  static constexpr int kCtas = NB == 1 ? 4 : NB <= 4 ? 2 : 1;  // CTAs an SM should hold
 };
-// tile t of the upper list: row block i, column tile j (of 8), j = 2i .. 2M - 1
-template <int M>
+// tile t of the list: row block i, column tile j (of 8), j = 2i .. NB - 1
+template <int NB>
 __device__ __forceinline__ void mu_tile(int t, int &i, int &j) {
   i = 0;
 #pragma unroll
-  for (int k = 0; k < M - 1; ++k)
-    if (i == k && t >= 2 * (M - k)) {
-      t -= 2 * (M - k);
+  for (int k = 0; k < MuF<NB>::M - 1; ++k)
+    if (i == k && t >= NB - 2 * k) {
+      t -= NB - 2 * k;
       i = k + 1;
     }
   j = 2 * i + t;
 }
-template <int RP>
-__device__ __forceinline__ int mu_at(int row, int col) { return row * RP + (col ^ ((row & 3) << 2)); }
+template <int NB>
+__device__ __forceinline__ int mu_at(int row, int col) { return row * MuF<NB>::RP + (col ^ ((row & 3) << 2)); }
 
 struct MuonFused {
   const float *g, *m;   // gradient and momentum in (m null: U = g)
@@ -391,65 +397,143 @@ struct MuonFused {
   int slice;            // columns per CTA, a multiple of 32
 };
 
-// this warp's tiles of A·B (symmetric commuting operands) in registers
-template <int RP>
-__device__ __forceinline__ void mu_product(const double *A, const double *B, int warp, int lane,
-                                           double (&acc)[MuF<RP>::kPerP][4]) {
+// One tile of A·B for symmetric commuting operands, of which the 16 x 16 blocks on
+// and above the diagonal are stored: a fragment of a block below it is read from its
+// mirror (as free of bank conflicts: lanes (g, t) at column g ^ 4t of row t).
+template <int NB>
+__device__ __forceinline__ void mu_tile_product(const double *A, const double *B, int i, int j, int lane,
+                                                double (&acc)[4]) {
+  constexpr int RP = MuF<NB>::RP;
   const int g = lane >> 2, t = lane & 3;
+  const int jb = j >> 1;
+  const int sw = (g & 3) << 2, tw = t << 2;
+  const double *a_row = A + (16 * i + g) * RP + t, *a_col = A + t * RP;
+  const double *b_row = B + (8 * j + g) * RP + t, *b_col = B + t * RP;
+  const int a_c0 = (16 * i + g) ^ tw, a_c1 = (16 * i + 8 + g) ^ tw, b_c = (8 * j + g) ^ tw;
 #pragma unroll
-  for (int q = 0; q < MuF<RP>::kPerP; ++q) {
+  for (int e = 0; e < 4; ++e) acc[e] = 0.0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[q][e] = 0.0;
-    const int tile = warp + 8 * q;
-    if (tile < MuF<RP>::kTiles) {
-      int i, j;
-      mu_tile<MuF<RP>::M>(tile, i, j);
-      const double *a0 = A + (16 * i + g) * RP, *a1 = a0 + 8 * RP, *b = B + (8 * j + g) * RP;
-      const int sw = (g & 3) << 2;
-#pragma unroll
-      for (int k = 0; k < RP; k += 4) {
-        const int o = (k ^ sw) + t;
-        dmma(acc[q], a0[o], a1[o], b[o]);
-      }
-    }
+  for (int k = 0; k < 8 * NB; k += 4) {
+    const bool up_a = (k >> 4) >= i, up_b = (k >> 4) >= jb;
+    const double a0 = *(up_a ? a_row + (k ^ sw) : a_col + k * RP + a_c0);
+    const double a1 = *(up_a ? a_row + 8 * RP + (k ^ sw) : a_col + k * RP + a_c1);
+    const double b = *(up_b ? b_row + (k ^ sw) : b_col + k * RP + b_c);
+    dmma(acc, a0, a1, b);
   }
 }
-// ... and to shared memory, with their mirrors; poly: c·acc + b·A + a·I instead
-template <int RP>
-__device__ __forceinline__ void mu_write(double *C, const double *A, bool poly, int rank, int warp, int lane,
-                                         const double (&acc)[MuF<RP>::kPerP][4]) {
+// ... and to shared memory; poly: c·acc + b·A + a·I instead
+template <int NB>
+__device__ __forceinline__ void mu_tile_write(double *C, const double *A, bool poly, int rank, int i, int j, int lane,
+                                              const double (&acc)[4]) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int q = 0; q < MuF<RP>::kPerP; ++q) {
-    const int tile = warp + 8 * q;
-    if (tile < MuF<RP>::kTiles) {
-      int i, j;
-      mu_tile<MuF<RP>::M>(tile, i, j);
+  for (int h = 0; h < 2; ++h) {
+    const int row = 16 * i + g + 8 * h, col = 8 * j + 2 * t;
+    const int o = mu_at<NB>(row, col);
+    double2 v = make_double2(acc[2 * h], acc[2 * h + 1]);
+    if (poly) {
+      const double2 b = *reinterpret_cast<const double2 *>(A + o);
+      v.x = kNsCd * v.x + kNsBd * b.x + (row == col && row < rank ? kNsAd : 0.0);
+      v.y = kNsCd * v.y + kNsBd * b.y + (row == col + 1 && row < rank ? kNsAd : 0.0);
+    }
+    *reinterpret_cast<double2 *>(C + o) = v;
+  }
+}
+// The five steps: G (scaled) and the working matrices Q, P; P holds the result.
+// 8 warps; a phase's tiles (of one product, or of two) are dealt to them.
+template <int NB>
+__device__ __forceinline__ void mu_iterate(double *G, double *Q, double *P, int rank, int warp, int lane) {
+  using F = MuF<NB>;
+#pragma unroll 1
+  for (int step = 0; step < kNsSteps; ++step) {
+    const bool last = step == kNsSteps - 1;
+    {
+      // Q = a·I + b·G + c·G·G (its last readers are behind a barrier); the first Q is P
+      double a[F::kPerP][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = 16 * i + g + (e >> 1) * 8, col = 8 * j + 2 * t + (e & 1);
-        double v = acc[q][e];
-        if (poly) v = kNsCd * v + kNsBd * A[mu_at<RP>(row, col)] + (row == col && row < rank ? kNsAd : 0.0);
-        C[mu_at<RP>(row, col)] = v;
-        if ((j >> 1) != i) C[mu_at<RP>(col, row)] = v;
+      for (int q = 0; q < F::kPerP; ++q) {
+        const int tile = warp + 8 * q;
+        if (tile < F::kTiles) {
+          int i, j;
+          mu_tile<NB>(tile, i, j);
+          mu_tile_product<NB>(G, G, i, j, lane, a[q]);
+          mu_tile_write<NB>(Q, G, true, rank, i, j, lane, a[q]);
+          if (step == 0) mu_tile_write<NB>(P, G, true, rank, i, j, lane, a[q]);
+        }
       }
+    }
+    __syncthreads();
+    {
+      // T = Q·G in G's place, P·Q in P's: written once every read is done
+      const int n_t = last ? 0 : F::kTiles, n = n_t + (step > 0 ? F::kTiles : 0);
+      double a[F::kPerP2][4];
+#pragma unroll
+      for (int q = 0; q < F::kPerP2; ++q) {
+        const int job = warp + 8 * q;
+        if (job < n) {
+          int i, j;
+          mu_tile<NB>(job < n_t ? job : job - n_t, i, j);
+          mu_tile_product<NB>(Q, job < n_t ? G : P, i, j, lane, a[q]);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < F::kPerP2; ++q) {
+        const int job = warp + 8 * q;
+        if (job < n) {
+          int i, j;
+          mu_tile<NB>(job < n_t ? job : job - n_t, i, j);
+          mu_tile_write<NB>(job < n_t ? G : P, nullptr, false, rank, i, j, lane, a[q]);
+        }
+      }
+      __syncthreads();
+    }
+    if (!last) {
+      double a[F::kPerP][4];  // G = Q·T
+#pragma unroll
+      for (int q = 0; q < F::kPerP; ++q) {
+        const int tile = warp + 8 * q;
+        if (tile < F::kTiles) {
+          int i, j;
+          mu_tile<NB>(tile, i, j);
+          mu_tile_product<NB>(Q, G, i, j, lane, a[q]);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < F::kPerP; ++q) {
+        const int tile = warp + 8 * q;
+        if (tile < F::kTiles) {
+          int i, j;
+          mu_tile<NB>(tile, i, j);
+          mu_tile_write<NB>(G, nullptr, false, rank, i, j, lane, a[q]);
+        }
+      }
+      __syncthreads();
     }
   }
 }
 
-template <int RP>
-__global__ void __launch_bounds__(256, MuF<RP>::kCtas)
+template <int NB>
+__global__ void __launch_bounds__(256, MuF<NB>::kCtas)
     lora_muon_fused_kernel(const MuonAdapter *__restrict__ ads, const int32_t *__restrict__ active, MuonFused p,
                            MuonOutput out) {
-  using F = MuF<RP>;
+  using F = MuF<NB>;
+  constexpr int RP = F::RP;
   extern __shared__ __align__(1024) uint8_t mu_smem[];
   double *mat = reinterpret_cast<double *>(mu_smem);
   float *us = reinterpret_cast<float *>(mu_smem + F::kMatBytes);
   uint32_t ncta, rank_in;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncta));
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank_in));
+  // the launches of one step work on different adapters: the next one may start
+  // once all of this one's CTAs run, and none ends before the one before it has
+  pdl_launch_dependents();
   const MuonAdapter ad = ads[blockIdx.x / ncta];
-  if (active && active[ad.index] == 0) return;  // the whole cluster
+  if (active && active[ad.index] == 0) {  // the whole cluster
+    pdl_wait();
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = ad.rank;
   const int64_t c0 = static_cast<int64_t>(rank_in) * p.slice;
@@ -458,7 +542,7 @@ __global__ void __launch_bounds__(256, MuF<RP>::kCtas)
 
   // ---- the slice's rows: momentum, U
   {
-    constexpr int kUn = 4;
+    constexpr int kUn = F::kUn;
     const int total = r * nc4;
     int row = 0, c = static_cast<int>(threadIdx.x);
     if (nc4 > 0) {
@@ -510,107 +594,90 @@ __global__ void __launch_bounds__(256, MuF<RP>::kCtas)
   }
   __syncthreads();
 
-  // ---- the slice's Gram matrix: warp = (k range, tiles); lane (g, t) needs the same
-  // values U[16 i + g (+ 8)][k + t] as A fragments and as B fragments
+  // ---- the slice's Gram matrix: each warp every eighth group of four columns, all
+  // tiles (lane (g, t) needs the same values U[8 b + g][k + t] as A and as B fragments)
   {
-    const int grp = warp % F::kGroups, ks = warp / F::kGroups;
     const int g = lane >> 2, t = lane & 3;
-    double acc[F::kPer][4] = {};
-    for (int kk = ks; kk < nc4; kk += F::kSplits) {
+    double acc[F::kTiles][4] = {};
+    for (int kk = warp; kk < nc4; kk += 8) {
       double v[2 * F::M];
 #pragma unroll
       for (int b = 0; b < 2 * F::M; ++b)
-        v[b] = 8 * b + g < r ? static_cast<double>(us[(8 * b + g) * p.slice + ((4 * kk) ^ (g << 2)) + t]) : 0.0;
+        v[b] = b < NB && 8 * b + g < r ? static_cast<double>(us[(8 * b + g) * p.slice + ((4 * kk) ^ (g << 2)) + t]) : 0.0;
+      int q = 0;
 #pragma unroll
-      for (int q = 0; q < F::kPer; ++q) {
-        const int tile = grp + F::kGroups * q;
-        if (F::kGroups == 1) {
-          dmma(acc[q], v[0], v[1], v[q]);  // RP = 16: tiles (0, 0), (0, 1)
-        } else if (tile < F::kTiles) {
-          int i, j;
-          mu_tile<F::M>(tile, i, j);
-          double a0 = 0.0, a1 = 0.0, bb = 0.0;
+      for (int i = 0; i < F::M; ++i)
 #pragma unroll
-          for (int b = 0; b < 2 * F::M; ++b) {  // (i, j differ per warp: select, no indexing)
-            if (b == 2 * i) a0 = v[b];
-            if (b == 2 * i + 1) a1 = v[b];
-            if (b == j) bb = v[b];
-          }
-          dmma(acc[q], a0, a1, bb);
+        for (int j = 2 * i; j < NB; ++j) dmma(acc[q++], v[2 * i], v[2 * i + 1], v[j]);
+    }
+    // the warps' sums, kBufs at a time: the upper half hands its sums to the lower one
+    double2 *buf = reinterpret_cast<double2 *>(mat + (warp % F::kBufs) * F::kPart) + lane;
+    if (F::kBufs == 4) {
+      if (warp >= 4) {
+#pragma unroll
+        for (int q = 0; q < F::kTiles; ++q) {
+          buf[(2 * q) * 32] = make_double2(acc[q][0], acc[q][1]);
+          buf[(2 * q + 1) * 32] = make_double2(acc[q][2], acc[q][3]);
+        }
+      }
+      __syncthreads();
+      if (warp < 4) {
+#pragma unroll
+        for (int q = 0; q < F::kTiles; ++q) {
+          const double2 x = buf[(2 * q) * 32], y = buf[(2 * q + 1) * 32];
+          acc[q][0] += x.x, acc[q][1] += x.y, acc[q][2] += y.x, acc[q][3] += y.y;
         }
       }
     }
-    double *red = mat + ks * F::kMat;
+    if (warp < F::kBufs) {  // (over its own buffer, which it alone has read)
 #pragma unroll
-    for (int q = 0; q < F::kPer; ++q) {
-      const int tile = grp + F::kGroups * q;
-      if (tile < F::kTiles) {
-        int i, j;
-        mu_tile<F::M>(tile, i, j);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          red[mu_at<RP>(16 * i + g + (e >> 1) * 8, 8 * j + 2 * t + (e & 1))] = acc[q][e];
+      for (int q = 0; q < F::kTiles; ++q) {
+        buf[(2 * q) * 32] = make_double2(acc[q][0], acc[q][1]);
+        buf[(2 * q + 1) * 32] = make_double2(acc[q][2], acc[q][3]);
       }
     }
   }
   __syncthreads();
-  // the k ranges' sums, in order (only the blocks on and above the diagonal were formed)
-  for (int e = threadIdx.x; e < F::kMat; e += 256) {
-    const int row = e / RP, col = e % RP;
-    if ((col >> 4) >= (row >> 4)) {
-      const int o = mu_at<RP>(row, col);
-      double v = mat[o];
-      for (int k = 1; k < F::kSplits; ++k) v += mat[k * F::kMat + o];
-      mat[o] = v;
-    }
+  for (int e = threadIdx.x; e < F::kPart; e += 256) {
+    double v = mat[e];
+#pragma unroll
+    for (int k = 1; k < F::kBufs; ++k) v += mat[k * F::kPart + e];
+    mat[e] = v;
   }
   if (ncta > 1) cluster_barrier();
   else __syncthreads();
-  float *pf = reinterpret_cast<float *>(mat + F::kMat);  // P as fp32 [RP][RP], in the second matrix's place
+  float *pf = reinterpret_cast<float *>(mat);  // P as fp32 [RP][RP], in Q's place
   if (rank_in == 0) {
     // ---- the first CTA: G0, the iteration, P
-    double *G = mat, *Q = mat + F::kMat, *P = mat + 2 * F::kMat;
-    for (int e = threadIdx.x; e < F::kMat; e += 256) {
-      const int row = e / RP, col = e % RP;
-      if ((col >> 4) >= (row >> 4)) {
-        const int o = mu_at<RP>(row, col);
-        double v = G[o];
-        for (uint32_t q = 1; q < ncta; ++q) v += ld_cluster_f64(map_rank(smem_u32(G + o), q));
-        G[o] = v;
-        if ((col >> 4) > (row >> 4)) G[mu_at<RP>(col, row)] = v;
-      }
+    static_assert(F::kPart <= 2 * F::kMat, "G's place is clear of the partial sums");
+    double *Q = mat, *P = mat + F::kMat, *G = mat + 2 * F::kMat;
+    for (int e = threadIdx.x; e < F::kPart; e += 256) {
+      double v = mat[e], w[7];
+#pragma unroll
+      for (uint32_t q = 1; q < 8; ++q) w[q - 1] = q < ncta ? ld_cluster_f64(map_rank(smem_u32(mat + e), q)) : 0.0;
+#pragma unroll
+      for (int q = 0; q < 7; ++q) v += w[q];
+      // element (e & 1) of half h of lane ln of tile q
+      const int ln = (e >> 1) & 31, h = (e >> 6) & 1;
+      int i, j;
+      mu_tile<NB>(e >> 7, i, j);
+      G[mu_at<NB>(16 * i + 8 * h + (ln >> 2), 8 * j + 2 * (ln & 3) + (e & 1))] = v;
     }
     __syncthreads();
     double tr = 0.0;
-    for (int i = lane; i < r; i += 32) tr += G[mu_at<RP>(i, i)];
+    for (int i = lane; i < r; i += 32) tr += G[mu_at<NB>(i, i)];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tr += __shfl_xor_sync(0xFFFFFFFFu, tr, o);
     const double inv = 1.0 / (sqrt(tr) + kNsEps);
     __syncthreads();
-    for (int e = threadIdx.x; e < F::kMat; e += 256) G[e] *= inv * inv;
+    for (int e = threadIdx.x; e < F::kMat; e += 256) G[e] *= inv * inv;  // (what is not part of a tile is never read)
     __syncthreads();
-    double a1[F::kPerP][4], a2[F::kPerP][4];
-#pragma unroll 1
-    for (int step = 0; step < kNsSteps; ++step) {
-      const bool last = step == kNsSteps - 1;
-      mu_product<RP>(G, G, warp, lane, a1);
-      mu_write<RP>(Q, G, true, r, warp, lane, a1);  // Q's last readers are behind a barrier
-      if (step == 0) mu_write<RP>(P, G, true, r, warp, lane, a1);  // the first Q is P
-      __syncthreads();
-      if (!last) mu_product<RP>(Q, G, warp, lane, a1);
-      if (step > 0) mu_product<RP>(P, Q, warp, lane, a2);
-      __syncthreads();  // every read of G and P is done: their products replace them
-      if (!last) mu_write<RP>(G, nullptr, false, r, warp, lane, a1);
-      if (step > 0) mu_write<RP>(P, nullptr, false, r, warp, lane, a2);
-      __syncthreads();
-      if (!last) {
-        mu_product<RP>(Q, G, warp, lane, a1);  // Q·(Q·G)
-        __syncthreads();
-        mu_write<RP>(G, nullptr, false, r, warp, lane, a1);
-        __syncthreads();
-      }
+    mu_iterate<NB>(G, Q, P, r, warp, lane);
+    for (int e = threadIdx.x; e < F::kMat; e += 256) {
+      const int row = e / RP, col = e % RP;
+      const bool up = (col >> 4) >= (row >> 4);
+      pf[e] = static_cast<float>(P[up ? mu_at<NB>(row, col) : mu_at<NB>(col, row)] * inv);
     }
-    for (int e = threadIdx.x; e < F::kMat; e += 256) pf[e] = static_cast<float>(P[mu_at<RP>(e / RP, e % RP)] * inv);
   }
   if (ncta > 1) {
     cluster_barrier();
@@ -632,6 +699,15 @@ __global__ void __launch_bounds__(256, MuF<RP>::kCtas)
     float4 acc[F::kRows];
 #pragma unroll
     for (int i = 0; i < F::kRows; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // (where registers allow, the weights are on their way while O is formed)
+    constexpr bool kEarly = NB >= 2 && F::kRows == 8;
+    float4 wv[kEarly ? 8 : 1];
+    if (kEarly && !out.O) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (grp * 8 + i < r) wv[kEarly ? i : 0] = *reinterpret_cast<const float4 *>(out.w + base + (grp * 8 + i) * p.d + c);
+    }
+#pragma unroll 4
     for (int k = 0; k < r; ++k) {
       const float4 u = *reinterpret_cast<const float4 *>(us + k * p.slice + (c ^ ((k & 7) << 2)));
       const float4 *pk = reinterpret_cast<const float4 *>(pf + k * RP + grp * F::kRows);
@@ -652,11 +728,15 @@ __global__ void __launch_bounds__(256, MuF<RP>::kCtas)
 #pragma unroll
     for (int i = 0; i < F::kRows; ++i) {
       const int row = grp * F::kRows + i;
-      if (row < r) muon_store4(out, base + row * p.d + c, step, acc[i]);
+      if (row < r) {
+        if (kEarly && !out.O) muon_store4(out, base + row * p.d + c, step, acc[i], wv[kEarly ? i : 0]);
+        else muon_store4(out, base + row * p.d + c, step, acc[i]);
+      }
     }
   }
   __syncwarp();
   if (ncta > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  pdl_wait();
 }
 
 }  // namespace lora
