@@ -372,6 +372,11 @@ struct MuF {
   static constexpr int kRows = NB <= 4 ? 8 : 16;       // rows per thread of the application
   static constexpr int kUn = NB == 1 ? 4 : 8;          // 16-byte loads in flight per thread and array
   static constexpr int kCtas = NB == 1 ? 4 : NB <= 4 ? 2 : 1;  // CTAs an SM should hold
+  // The iteration: above rank 32 the cluster's CTAs share each product's tiles (rank
+  // 64: 65,000 cycles in one CTA, bound by its fp64 MMAs); below it one CTA iterates
+  // (a cluster barrier costs more than a product of rank 32).
+  static constexpr bool kShared = NB >= 5;
+  static constexpr int kCols4 = NB >= 5 ? 2 : 1;       // 4-column groups per thread of the application
 };
 // tile t of the list: row block i, column tile j (of 8), j = 2i .. NB - 1
 template <int NB>
@@ -424,7 +429,7 @@ __device__ __forceinline__ void mu_tile_product(const double *A, const double *B
 // ... and to shared memory; poly: c·acc + b·A + a·I instead
 template <int NB>
 __device__ __forceinline__ void mu_tile_write(double *C, const double *A, bool poly, int rank, int i, int j, int lane,
-                                              const double (&acc)[4]) {
+                                              const double (&acc)[4], uint32_t ncta) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -436,14 +441,28 @@ __device__ __forceinline__ void mu_tile_write(double *C, const double *A, bool p
       v.x = kNsCd * v.x + kNsBd * b.x + (row == col && row < rank ? kNsAd : 0.0);
       v.y = kNsCd * v.y + kNsBd * b.y + (row == col + 1 && row < rank ? kNsAd : 0.0);
     }
-    *reinterpret_cast<double2 *>(C + o) = v;
+    if constexpr (MuF<NB>::kShared) {
+      const uint32_t a = smem_u32(C + o);
+      for (uint32_t q = 0; q < ncta; ++q)
+        asm volatile("st.shared::cluster.v2.f64 [%0], {%1, %2};" ::"r"(map_rank(a, q)), "d"(v.x), "d"(v.y) : "memory");
+    } else {
+      *reinterpret_cast<double2 *>(C + o) = v;
+    }
   }
 }
 // The five steps: G (scaled) and the working matrices Q, P; P holds the result.
-// 8 warps; a phase's tiles (of one product, or of two) are dealt to them.
+// A phase's tiles (of one product, or of two) are dealt to the 8 warps, or to those of
+// all CTAs (kShared: each CTA holds all three matrices and writes its tiles to all).
 template <int NB>
-__device__ __forceinline__ void mu_iterate(double *G, double *Q, double *P, int rank, int warp, int lane) {
+__device__ __forceinline__ void mu_iterate(double *G, double *Q, double *P, int rank, int warp, int lane,
+                                           uint32_t cta, uint32_t ncta) {
   using F = MuF<NB>;
+  const int first = F::kShared ? static_cast<int>(cta + ncta * warp) : warp;
+  const int stride = F::kShared ? static_cast<int>(8 * ncta) : 8;
+  auto sync = [&]() {
+    if constexpr (F::kShared) cluster_barrier();
+    else __syncthreads();
+  };
 #pragma unroll 1
   for (int step = 0; step < kNsSteps; ++step) {
     const bool last = step == kNsSteps - 1;
@@ -452,64 +471,64 @@ __device__ __forceinline__ void mu_iterate(double *G, double *Q, double *P, int 
       double a[F::kPerP][4];
 #pragma unroll
       for (int q = 0; q < F::kPerP; ++q) {
-        const int tile = warp + 8 * q;
+        const int tile = first + stride * q;
         if (tile < F::kTiles) {
           int i, j;
           mu_tile<NB>(tile, i, j);
           mu_tile_product<NB>(G, G, i, j, lane, a[q]);
-          mu_tile_write<NB>(Q, G, true, rank, i, j, lane, a[q]);
-          if (step == 0) mu_tile_write<NB>(P, G, true, rank, i, j, lane, a[q]);
+          mu_tile_write<NB>(Q, G, true, rank, i, j, lane, a[q], ncta);
+          if (step == 0) mu_tile_write<NB>(P, G, true, rank, i, j, lane, a[q], ncta);
         }
       }
     }
-    __syncthreads();
+    sync();
     {
       // T = Q·G in G's place, P·Q in P's: written once every read is done
       const int n_t = last ? 0 : F::kTiles, n = n_t + (step > 0 ? F::kTiles : 0);
       double a[F::kPerP2][4];
 #pragma unroll
       for (int q = 0; q < F::kPerP2; ++q) {
-        const int job = warp + 8 * q;
+        const int job = first + stride * q;
         if (job < n) {
           int i, j;
           mu_tile<NB>(job < n_t ? job : job - n_t, i, j);
           mu_tile_product<NB>(Q, job < n_t ? G : P, i, j, lane, a[q]);
         }
       }
-      __syncthreads();
+      sync();
 #pragma unroll
       for (int q = 0; q < F::kPerP2; ++q) {
-        const int job = warp + 8 * q;
+        const int job = first + stride * q;
         if (job < n) {
           int i, j;
           mu_tile<NB>(job < n_t ? job : job - n_t, i, j);
-          mu_tile_write<NB>(job < n_t ? G : P, nullptr, false, rank, i, j, lane, a[q]);
+          mu_tile_write<NB>(job < n_t ? G : P, nullptr, false, rank, i, j, lane, a[q], ncta);
         }
       }
-      __syncthreads();
+      sync();
     }
     if (!last) {
       double a[F::kPerP][4];  // G = Q·T
 #pragma unroll
       for (int q = 0; q < F::kPerP; ++q) {
-        const int tile = warp + 8 * q;
+        const int tile = first + stride * q;
         if (tile < F::kTiles) {
           int i, j;
           mu_tile<NB>(tile, i, j);
           mu_tile_product<NB>(Q, G, i, j, lane, a[q]);
         }
       }
-      __syncthreads();
+      sync();
 #pragma unroll
       for (int q = 0; q < F::kPerP; ++q) {
-        const int tile = warp + 8 * q;
+        const int tile = first + stride * q;
         if (tile < F::kTiles) {
           int i, j;
           mu_tile<NB>(tile, i, j);
-          mu_tile_write<NB>(G, nullptr, false, rank, i, j, lane, a[q]);
+          mu_tile_write<NB>(G, nullptr, false, rank, i, j, lane, a[q], ncta);
         }
       }
-      __syncthreads();
+      sync();
     }
   }
 }
@@ -647,23 +666,24 @@ __global__ void __launch_bounds__(256, MuF<NB>::kCtas)
   if (ncta > 1) cluster_barrier();
   else __syncthreads();
   float *pf = reinterpret_cast<float *>(mat);  // P as fp32 [RP][RP], in Q's place
-  if (rank_in == 0) {
-    // ---- the first CTA: G0, the iteration, P
+  if (F::kShared || rank_in == 0) {
+    // ---- G0, the iteration, P: every CTA (kShared) or the cluster's first
     static_assert(F::kPart <= 2 * F::kMat, "G's place is clear of the partial sums");
     double *Q = mat, *P = mat + F::kMat, *G = mat + 2 * F::kMat;
     for (int e = threadIdx.x; e < F::kPart; e += 256) {
-      double v = mat[e], w[7];
+      double w[8], v = 0.0;
 #pragma unroll
-      for (uint32_t q = 1; q < 8; ++q) w[q - 1] = q < ncta ? ld_cluster_f64(map_rank(smem_u32(mat + e), q)) : 0.0;
+      for (uint32_t q = 0; q < 8; ++q) w[q] = q < ncta ? ld_cluster_f64(map_rank(smem_u32(mat + e), q)) : 0.0;
 #pragma unroll
-      for (int q = 0; q < 7; ++q) v += w[q];
+      for (int q = 0; q < 8; ++q) v += w[q];
       // element (e & 1) of half h of lane ln of tile q
       const int ln = (e >> 1) & 31, h = (e >> 6) & 1;
       int i, j;
       mu_tile<NB>(e >> 7, i, j);
       G[mu_at<NB>(16 * i + 8 * h + (ln >> 2), 8 * j + 2 * (ln & 3) + (e & 1))] = v;
     }
-    __syncthreads();
+    if (F::kShared) cluster_barrier();  // the partial sums are read: Q may take their place
+    else __syncthreads();
     double tr = 0.0;
     for (int i = lane; i < r; i += 32) tr += G[mu_at<NB>(i, i)];
 #pragma unroll
@@ -672,14 +692,14 @@ __global__ void __launch_bounds__(256, MuF<NB>::kCtas)
     __syncthreads();
     for (int e = threadIdx.x; e < F::kMat; e += 256) G[e] *= inv * inv;  // (what is not part of a tile is never read)
     __syncthreads();
-    mu_iterate<NB>(G, Q, P, r, warp, lane);
+    mu_iterate<NB>(G, Q, P, r, warp, lane, rank_in, ncta);
     for (int e = threadIdx.x; e < F::kMat; e += 256) {
       const int row = e / RP, col = e % RP;
       const bool up = (col >> 4) >= (row >> 4);
       pf[e] = static_cast<float>(P[up ? mu_at<NB>(row, col) : mu_at<NB>(col, row)] * inv);
     }
   }
-  if (ncta > 1) {
+  if (!F::kShared && ncta > 1) {
     cluster_barrier();
     if (rank_in != 0) {
       const uint32_t src = map_rank(smem_u32(pf), 0);
@@ -690,15 +710,19 @@ __global__ void __launch_bounds__(256, MuF<NB>::kCtas)
   }
   __syncthreads();
 
-  // ---- O = P·U of the slice: kRows rows x 4 columns per thread (P is symmetric: row k
-  // holds column k)
+  // ---- O = P·U of the slice: kRows rows x kCols4 groups of 4 columns per thread (P is
+  // symmetric: row k holds column k)
   const float step = muon_step_size(out, r, p.d);
   const int ngrp = (r + F::kRows - 1) / F::kRows;
-  for (int e = threadIdx.x; e < ngrp * nc4; e += 256) {
-    const int grp = e / nc4, c = 4 * (e - grp * nc4);
-    float4 acc[F::kRows];
+  const int nc = (nc4 + F::kCols4 - 1) / F::kCols4;
+  for (int e = threadIdx.x; e < ngrp * nc; e += 256) {
+    const int grp = e / nc;
+    const int c = 4 * (e - grp * nc);
+    float4 acc[F::kCols4][F::kRows];
 #pragma unroll
-    for (int i = 0; i < F::kRows; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int h = 0; h < F::kCols4; ++h)
+#pragma unroll
+      for (int i = 0; i < F::kRows; ++i) acc[h][i] = make_float4(0.f, 0.f, 0.f, 0.f);
     // (where registers allow, the weights are on their way while O is formed)
     constexpr bool kEarly = NB >= 2 && F::kRows == 8;
     float4 wv[kEarly ? 8 : 1];
@@ -707,9 +731,15 @@ __global__ void __launch_bounds__(256, MuF<NB>::kCtas)
       for (int i = 0; i < 8; ++i)
         if (grp * 8 + i < r) wv[kEarly ? i : 0] = *reinterpret_cast<const float4 *>(out.w + base + (grp * 8 + i) * p.d + c);
     }
-#pragma unroll 4
+#pragma unroll 2
     for (int k = 0; k < r; ++k) {
-      const float4 u = *reinterpret_cast<const float4 *>(us + k * p.slice + (c ^ ((k & 7) << 2)));
+      float4 u[F::kCols4];
+#pragma unroll
+      for (int h = 0; h < F::kCols4; ++h) {
+        // (a second group past the slice's columns reads inside the row and is not stored)
+        const int ch = min(c + 4 * h * nc, p.slice - 4);
+        u[h] = *reinterpret_cast<const float4 *>(us + k * p.slice + (ch ^ ((k & 7) << 2)));
+      }
       const float4 *pk = reinterpret_cast<const float4 *>(pf + k * RP + grp * F::kRows);
 #pragma unroll
       for (int i4 = 0; i4 < F::kRows / 4; ++i4) {
@@ -717,25 +747,33 @@ __global__ void __launch_bounds__(256, MuF<NB>::kCtas)
         const float av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float4 &o = acc[4 * i4 + i];
-          o.x = fmaf(av[i], u.x, o.x);
-          o.y = fmaf(av[i], u.y, o.y);
-          o.z = fmaf(av[i], u.z, o.z);
-          o.w = fmaf(av[i], u.w, o.w);
+#pragma unroll
+          for (int h = 0; h < F::kCols4; ++h) {
+            float4 &o = acc[h][4 * i4 + i];
+            o.x = fmaf(av[i], u[h].x, o.x);
+            o.y = fmaf(av[i], u[h].y, o.y);
+            o.z = fmaf(av[i], u[h].z, o.z);
+            o.w = fmaf(av[i], u[h].w, o.w);
+          }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < F::kRows; ++i) {
-      const int row = grp * F::kRows + i;
-      if (row < r) {
-        if (kEarly && !out.O) muon_store4(out, base + row * p.d + c, step, acc[i], wv[kEarly ? i : 0]);
-        else muon_store4(out, base + row * p.d + c, step, acc[i]);
+    for (int h = 0; h < F::kCols4; ++h) {
+      if (c + 4 * h * nc >= 4 * nc4) break;
+#pragma unroll
+      for (int i = 0; i < F::kRows; ++i) {
+        const int row = grp * F::kRows + i;
+        if (row < r) {
+          const int64_t o = base + row * p.d + c + 4 * h * nc;
+          if (kEarly && !out.O) muon_store4(out, o, step, acc[h][i], wv[kEarly ? i : 0]);
+          else muon_store4(out, o, step, acc[h][i]);
+        }
       }
     }
   }
   __syncwarp();
-  if (ncta > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (!F::kShared && ncta > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   pdl_wait();
 }
 
