@@ -131,7 +131,7 @@ def _check(rc: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # (argtypes make it a pointer)
 
 
 _BF16 = ("bfloat16",)
@@ -140,6 +140,7 @@ _I32 = ("int32", "uint32")
 _FP8 = ("float8_e4m3fn", "uint8")  # e4m3 values, or their bytes
 
 
+_DTYPE_OK = set()  # (torch dtype, names it was accepted for)
 _DTYPE_NAME = {}  # torch dtype -> its short name ("bfloat16", ...), filled as dtypes are seen
 
 
@@ -153,8 +154,24 @@ def _dtype_name(dt):
 def _args(what, *specs):
     """Check (name, tensor, shape, dtype names, optional) for each tensor handed
     to the library call `what`: first every tensor's shape, dtype and layout,
-    then every tensor's device. (Called on every launch: the checks use the
-    cheapest accessors, a cached dtype name and the device index as an int.)"""
+    then every tensor's device. (Called on every launch: one pass of the cheapest
+    accessors first; the pass that names what is wrong runs only when that fails.)"""
+    import torch
+    dev = -2
+    for _, t, shape, dtypes, optional in specs:
+        if t is None:
+            if optional:
+                continue
+            break
+        if t.shape != shape or (t.dtype, dtypes) not in _DTYPE_OK or not t.is_contiguous():
+            break
+        idx = t.get_device()
+        if idx != dev:
+            if idx < 0 or dev >= 0 or idx != torch.cuda.current_device():
+                break
+            dev = idx
+    else:
+        return
     given = []
     for name, t, shape, dtypes, optional in specs:
         if t is None:
@@ -165,6 +182,7 @@ def _args(what, *specs):
             raise LoraError(-1, f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if _dtype_name(t.dtype) not in dtypes:
             raise LoraError(-1, f"{what}: {name} has dtype {t.dtype}, expected {' or '.join(dtypes)}")
+        _DTYPE_OK.add((t.dtype, dtypes))
         if not t.is_contiguous():
             raise LoraError(-1, f"{what}: {name} is not contiguous")
         given.append((name, t))
@@ -174,7 +192,6 @@ def _args(what, *specs):
         if idx < 0:
             raise LoraError(-1, f"{what}: {name} is not a CUDA tensor")
         if dev is None:
-            import torch
             dev = torch.cuda.current_device()
         if idx != dev:
             raise LoraError(-1, f"{what}: {name} is on {t.device}, the current device is cuda:{dev}")
@@ -183,10 +200,10 @@ def _args(what, *specs):
 def _stream(stream):
     if stream is None:
         import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        # the raw handle costs 0.1 us, a Stream object 3 us: a quarter of a small call
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _host_i32(a):

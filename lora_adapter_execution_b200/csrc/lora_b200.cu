@@ -84,7 +84,9 @@ int device_state(DeviceState **out) {
                                      sk_smem(4)) == cudaSuccess;
           ok &= cudaFuncSetAttribute(lora_shrink_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      sk_smem(2)) == cudaSuccess;
-          ok &= cudaFuncSetAttribute(lora_tcontract_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+          ok &= cudaFuncSetAttribute(lora_tcontract_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     tc_smem(kTcMaxR)) == cudaSuccess;
+          ok &= cudaFuncSetAttribute(lora_tcontract_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      tc_smem(kTcMaxR)) == cudaSuccess;
           ok &= qr_kernel_attributes();
           ok &= fp8_kernel_attributes();
@@ -744,9 +746,10 @@ void lora_plan_destroy(lora_plan_t plan) {
   delete plan;
 }
 
-int lora_linear_shrink(lora_plan_t plan, const uint16_t *X, const uint16_t *A_pool, const float *scale,
-                       double p_drop, uint64_t seed, float *U_save, const uint32_t *keep_bits,
-                       lora_stream_t stream) {
+namespace {
+// lora_linear_shrink; gathered: the plan's sorted copy of X is already in its scratch.
+int shrink_run(lora_plan_t plan, const uint16_t *X, bool gathered, const uint16_t *A_pool, const float *scale,
+               double p_drop, uint64_t seed, float *U_save, const uint32_t *keep_bits, lora_stream_t stream) {
   if (!plan || !plan->dev || !X || !A_pool || !scale) return LORA_ERR_ARG;
   if (!on_plan_device(plan)) return LORA_ERR_ARG;
   if (!aligned16(X) || !aligned16(A_pool)) return LORA_ERR_ARG;
@@ -789,7 +792,7 @@ int lora_linear_shrink(lora_plan_t plan, const uint16_t *X, const uint16_t *A_po
   sp.x_sorted = Xs ? 1 : 0;
   sp.U_save = U_save;
   sp.r_max = hp.r_max;
-  if (Xs) {
+  if (Xs && !gathered) {
     // sorted copy of X first (the shrink and the fused GEMM read token tiles from it)
     const int64_t pieces = hp.T * (hp.d_in / 8);
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((pieces + 255) / 256, 8 * ds->num_sms));
@@ -797,6 +800,13 @@ int lora_linear_shrink(lora_plan_t plan, const uint16_t *X, const uint16_t *A_po
     if (cudaGetLastError() != cudaSuccess) return LORA_ERR_CUDA;
   }
   return launch_unit_shrink(ds, plan, mX16, mA16, mBits16, sp, stream);
+}
+}  // namespace
+
+int lora_linear_shrink(lora_plan_t plan, const uint16_t *X, const uint16_t *A_pool, const float *scale,
+                       double p_drop, uint64_t seed, float *U_save, const uint32_t *keep_bits,
+                       lora_stream_t stream) {
+  return shrink_run(plan, X, false, A_pool, scale, p_drop, seed, U_save, keep_bits, stream);
 }
 
 int lora_fused_gemm(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const uint16_t *B_pool, uint16_t *Y,
@@ -1238,7 +1248,7 @@ int lora_linear_bwd(const uint16_t *X, const uint16_t *W, const uint16_t *A, con
       tp.partial = pdB;
       dim3 grid_b(static_cast<unsigned>((d_out + kTcCols - 1) / kTcCols), static_cast<unsigned>(S));
       const int smem_b = tc_smem(w);
-      lora_tcontract_kernel<<<grid_b, kTcThreads, smem_b, stream>>>(mdY64, mU, mBits, mU, mU, mU, tp);
+      lora_tcontract_kernel<false><<<grid_b, kTcThreads, smem_b, stream>>>(mdY64, mU, mBits, mU, mU, mU, tp);
       tp.N = static_cast<int32_t>(d_in);
       tp.thr = thr;
       tp.seed = seed;
@@ -1248,7 +1258,7 @@ int lora_linear_bwd(const uint16_t *X, const uint16_t *W, const uint16_t *A, con
       tp.wpr = (d_in + 31) / 32;
       tp.partial = pdA;
       dim3 grid_a(static_cast<unsigned>((d_in + kTcCols - 1) / kTcCols), static_cast<unsigned>(S));
-      lora_tcontract_kernel<<<grid_a, kTcThreads, smem_a, stream>>>(mX64, mdU, mBits, mdU, mdU, mdU, tp);
+      lora_tcontract_kernel<false><<<grid_a, kTcThreads, smem_a, stream>>>(mX64, mdU, mBits, mdU, mdU, mdU, tp);
     }
     const int64_t nb = static_cast<int64_t>(r) * d_out;
     const int64_t na = static_cast<int64_t>(r) * d_in;
@@ -1309,9 +1319,12 @@ struct Fp8Base {
   const uint8_t *Wq;
   const float *Sw;
 };
-int fp8_bwd_dx(DeviceState *ds, const lora_plan *plan, const Fp8Base &f8, const uint16_t *dY, const uint16_t *A_pool,
-               const uint8_t *img, uint16_t *dX, uint64_t seed, uint64_t thr, float inv_keep, const uint32_t *bits,
-               uint8_t *ws, lora_stream_t stream);  // fp8_api.inc
+int fp8_bwd_prep(DeviceState *ds, const lora_plan *plan, const uint16_t *dY, uint16_t *dYs, const uint16_t *X,
+                 uint16_t *Xs, const uint32_t *bits, uint32_t *bits_s, const float *U, float *Us, int rp, uint8_t *ws,
+                 lora_stream_t stream);  // fp8_api.inc
+int fp8_bwd_dx(DeviceState *ds, const lora_plan *plan, const Fp8Base &f8, const uint16_t *A_pool, const uint8_t *img,
+               uint16_t *dX, uint64_t seed, uint64_t thr, float inv_keep, const uint32_t *bits, uint8_t *ws,
+               lora_stream_t stream);  // fp8_api.inc
 
 // lora_linear_bwd_multi, over the bf16 base W or, with f8 given, the 8-bit one
 // (whose quantised dY lives behind the bf16 backward's workspace).
@@ -1362,20 +1375,28 @@ int bwd_multi_run(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const 
   auto grid_for = [&](int64_t n) {
     return static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 16 * ds->num_sms));
   };
-  // sorted copies of X, dY (and the keep bits) when the plan's tiles are not runs
-  if (gathers) {
-    lora_gather_rows_kernel<<<grid_for(T * (d_in / 8)), 256, 0, stream>>>(X, plan->d_perm,
-                                                                         const_cast<uint16_t *>(Xr), T, d_in);
-    lora_gather_rows_kernel<<<grid_for(T * (d_out / 8)), 256, 0, stream>>>(dY, plan->d_perm,
-                                                                          const_cast<uint16_t *>(dYr), T, d_out);
-    if (bits_tc)
-      lora_gather_rows_kernel<<<grid_for(T * wpr / 4), 256, 0, stream>>>(
-          reinterpret_cast<const uint16_t *>(bits), plan->d_perm,
-          reinterpret_cast<uint16_t *>(const_cast<uint32_t *>(bits_in)), T, 2 * wpr);
+  if (f8) {
+    rc = fp8_bwd_prep(ds, plan, dY, gathers ? const_cast<uint16_t *>(dYr) : nullptr, X,
+                      gathers ? const_cast<uint16_t *>(Xr) : nullptr, bits,
+                      gathers && bits_tc ? const_cast<uint32_t *>(bits_in) : nullptr, U_save, Us, rp, ws + Lw.total,
+                      stream);
+    if (rc != LORA_OK) return rc;
+  } else {
+    // sorted copies of X, dY (and the keep bits) when the plan's tiles are not runs
+    if (gathers) {
+      lora_gather_rows_kernel<<<grid_for(T * (d_in / 8)), 256, 0, stream>>>(X, plan->d_perm,
+                                                                           const_cast<uint16_t *>(Xr), T, d_in);
+      lora_gather_rows_kernel<<<grid_for(T * (d_out / 8)), 256, 0, stream>>>(dY, plan->d_perm,
+                                                                            const_cast<uint16_t *>(dYr), T, d_out);
+      if (bits_tc)
+        lora_gather_rows_kernel<<<grid_for(T * wpr / 4), 256, 0, stream>>>(
+            reinterpret_cast<const uint16_t *>(bits), plan->d_perm,
+            reinterpret_cast<uint16_t *>(const_cast<uint32_t *>(bits_in)), T, 2 * wpr);
+    }
+    // U in sorted order, rows padded to rp
+    lora_gather_pad_kernel<<<grid_for(T * rp), 256, 0, stream>>>(U_save, hp.r_max, plan->d_perm, Us, rp, T);
+    if (cudaGetLastError() != cudaSuccess) return LORA_ERR_CUDA;
   }
-  // U in sorted order, rows padded to rp
-  lora_gather_pad_kernel<<<grid_for(T * rp), 256, 0, stream>>>(U_save, hp.r_max, plan->d_perm, Us, rp, T);
-  if (cudaGetLastError() != cudaSuccess) return LORA_ERR_CUDA;
 
   // dU: the plan's shrink units over dY against B_pool: s_a·dU images (hi/lo,
   // the dX GEMM's adapter operand) and G = dY·B_a^T in sorted order
@@ -1400,7 +1421,7 @@ int bwd_multi_run(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const 
   // K-major operand, the adapter blocks A_pool rows (into a second accumulator,
   // masked in the epilogue, when there is dropout)
   if (f8) {
-    rc = fp8_bwd_dx(ds, plan, *f8, dY, A_pool, img, dX, seed, thr, inv_keep, bits, ws + Lw.total, stream);
+    rc = fp8_bwd_dx(ds, plan, *f8, A_pool, img, dX, seed, thr, inv_keep, bits, ws + Lw.total, stream);
     if (rc != LORA_OK) return rc;
   } else {
     CUtensorMap mdY128, mWt, mAl;
@@ -1484,7 +1505,8 @@ int bwd_multi_run(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const 
     tp.out = dB_pool;
     tp.partial = pdB;
     dim3 grid_b(static_cast<unsigned>((d_out + kTcCols - 1) / kTcCols), n_ranges, groups);
-    lora_tcontract_kernel<<<grid_b, kTcThreads, smem, stream>>>(mIn64b, mU[3], mBits, mU[0], mU[1], mU[2], tp);
+    const auto contract = f8 ? lora_tcontract_kernel<true> : lora_tcontract_kernel<false>;
+    contract<<<grid_b, kTcThreads, smem, stream>>>(mIn64b, mU[3], mBits, mU[0], mU[1], mU[2], tp);
     // dA: In = X with the dropout mask, G = dY·B^T; the mask's 1/(1 - p) and s_a
     // scale the sums
     tp.N = static_cast<int32_t>(d_in);
@@ -1497,7 +1519,7 @@ int bwd_multi_run(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const 
     tp.out = dA_pool;
     tp.partial = pdA;
     dim3 grid_a(static_cast<unsigned>((d_in + kTcCols - 1) / kTcCols), n_ranges, groups);
-    lora_tcontract_kernel<<<grid_a, kTcThreads, smem, stream>>>(mIn64a, mG[3], mBits, mG[0], mG[1], mG[2], tp);
+    contract<<<grid_a, kTcThreads, smem, stream>>>(mIn64a, mG[3], mBits, mG[0], mG[1], mG[2], tp);
     if (hp.partial_rows > 0) {
       const unsigned gb = static_cast<unsigned>(std::min<int64_t>((hp.r_max * d_out + 255) / 256, 256));
       const unsigned ga = static_cast<unsigned>(std::min<int64_t>((hp.r_max * d_in + 255) / 256, 256));
