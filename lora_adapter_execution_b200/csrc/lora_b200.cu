@@ -84,6 +84,10 @@ int device_state(DeviceState **out) {
                                      sk_smem(4)) == cudaSuccess;
           ok &= cudaFuncSetAttribute(lora_shrink_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      sk_smem(2)) == cudaSuccess;
+          ok &= cudaFuncSetAttribute(lora_shrink_kernel<4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     sk_smem(4)) == cudaSuccess;
+          ok &= cudaFuncSetAttribute(lora_shrink_kernel<2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     sk_smem(2)) == cudaSuccess;
           ok &= cudaFuncSetAttribute(lora_tcontract_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      tc_smem(kTcMaxR)) == cudaSuccess;
           ok &= cudaFuncSetAttribute(lora_tcontract_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -388,10 +392,10 @@ bool on_plan_device(const lora_plan *pl) {
 
 // The shrink over the plan's units (one CTA cluster per unit): In rows by mIn
 // (box {64, 16}), factor rows by mF (box {64, 16}), sp.K the contraction length;
-// the caller fills the rest of sp (scale, mask, outputs). Launched with
-// programmatic stream serialization.
+// the caller fills the rest of sp (scale, mask, outputs); fresh: the sums to fp32
+// (shrink_consume). Launched with programmatic stream serialization.
 int launch_unit_shrink(DeviceState *ds, const lora_plan *plan, const CUtensorMap &mIn, const CUtensorMap &mF,
-                       const CUtensorMap &mBits, ShrinkParams sp, lora_stream_t stream) {
+                       const CUtensorMap &mBits, ShrinkParams sp, bool fresh, lora_stream_t stream) {
   const HostPlan &hp = plan->hp;
   sp.mode = 0;
   sp.T = static_cast<int32_t>(hp.T);
@@ -426,8 +430,9 @@ int launch_unit_shrink(DeviceState *ds, const lora_plan *plan, const CUtensorMap
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, max_nb16 <= 2 ? lora_shrink_kernel<2> : lora_shrink_kernel<4>, mIn, mF, mBits,
-                         sp) != cudaSuccess) {
+  const auto kernel = max_nb16 <= 2 ? (fresh ? lora_shrink_kernel<2, true> : lora_shrink_kernel<2>)
+                                    : (fresh ? lora_shrink_kernel<4, true> : lora_shrink_kernel<4>);
+  if (cudaLaunchKernelEx(&cfg, kernel, mIn, mF, mBits, sp) != cudaSuccess) {
     cudaGetLastError();
     return LORA_ERR_CUDA;
   }
@@ -747,8 +752,9 @@ void lora_plan_destroy(lora_plan_t plan) {
 }
 
 namespace {
-// lora_linear_shrink; gathered: the plan's sorted copy of X is already in its scratch.
-int shrink_run(lora_plan_t plan, const uint16_t *X, bool gathered, const uint16_t *A_pool, const float *scale,
+// lora_linear_shrink; fp8: for the layer over the 8-bit base, whose caller has put the
+// plan's sorted copy of X (if it gathers) into the scratch already.
+int shrink_run(lora_plan_t plan, const uint16_t *X, bool fp8, const uint16_t *A_pool, const float *scale,
                double p_drop, uint64_t seed, float *U_save, const uint32_t *keep_bits, lora_stream_t stream) {
   if (!plan || !plan->dev || !X || !A_pool || !scale) return LORA_ERR_ARG;
   if (!on_plan_device(plan)) return LORA_ERR_ARG;
@@ -792,14 +798,14 @@ int shrink_run(lora_plan_t plan, const uint16_t *X, bool gathered, const uint16_
   sp.x_sorted = Xs ? 1 : 0;
   sp.U_save = U_save;
   sp.r_max = hp.r_max;
-  if (Xs && !gathered) {
+  if (Xs && !fp8) {
     // sorted copy of X first (the shrink and the fused GEMM read token tiles from it)
     const int64_t pieces = hp.T * (hp.d_in / 8);
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((pieces + 255) / 256, 8 * ds->num_sms));
     lora_gather_rows_kernel<<<blocks, 256, 0, stream>>>(X, plan->d_perm, Xs, hp.T, hp.d_in);
     if (cudaGetLastError() != cudaSuccess) return LORA_ERR_CUDA;
   }
-  return launch_unit_shrink(ds, plan, mX16, mA16, mBits16, sp, stream);
+  return launch_unit_shrink(ds, plan, mX16, mA16, mBits16, sp, fp8, stream);
 }
 }  // namespace
 
@@ -1414,7 +1420,7 @@ int bwd_multi_run(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const 
     sp.U_save = G;
     sp.r_max = rp;
     sp.u_sorted = 1;
-    rc = launch_unit_shrink(ds, plan, mdY16, mB16, mdY16, sp, stream);
+    rc = launch_unit_shrink(ds, plan, mdY16, mB16, mdY16, sp, f8 != nullptr, stream);
     if (rc != LORA_OK) return rc;
   }
   // dX = dY·W^T + D ⊙ (s_a·dU·A_a^T): the fused GEMM over the plan's tiles, W^T a

@@ -213,7 +213,10 @@ constexpr int kSkConsumerBar = 1;  // named barrier of the 256 consumer threads
 // the same for every stage (128-byte swizzle, 1024-byte aligned stage parts),
 // so they are computed once. After the last stage the warp writes its partial
 // sums to red[warp][slot * 16 + row][col] in the freed stage pool.
-template <int NB16>
+// kFresh: each MMA starts from zero and its sums are added by fp32 additions, rounded to
+// nearest, where the MMA's own accumulation truncates (over 4096 columns the error falls
+// from 1.0e-6 of the sums' size to 1.5e-7). Used by the layer over the 8-bit base.
+template <int NB16, bool kFresh>
 __device__ __forceinline__ void shrink_consume(const ShrinkWarp &w, const ShrinkParams &p, const UnitGeom &g,
                                                const int64_t (&orow)[2][2], const uint8_t *smem,
                                                volatile int *abort_flag, float *red, int warp, int lane) {
@@ -301,8 +304,19 @@ __device__ __forceinline__ void shrink_consume(const ShrinkWarp &w, const Shrink
         }
 #pragma unroll
         for (int jj = 0; jj < NB16; ++jj) {
-          mma_bf16_16816(acc[i][2 * jj], a0, a1, a2, a3, bf[jj][0], bf[jj][1]);
-          mma_bf16_16816(acc[i][2 * jj + 1], a0, a1, a2, a3, bf[jj][2], bf[jj][3]);
+          if constexpr (kFresh) {
+            float f0[4] = {0.f, 0.f, 0.f, 0.f}, f1[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_bf16_16816(f0, a0, a1, a2, a3, bf[jj][0], bf[jj][1]);
+            mma_bf16_16816(f1, a0, a1, a2, a3, bf[jj][2], bf[jj][3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[i][2 * jj][e] += f0[e];
+              acc[i][2 * jj + 1][e] += f1[e];
+            }
+          } else {
+            mma_bf16_16816(acc[i][2 * jj], a0, a1, a2, a3, bf[jj][0], bf[jj][1]);
+            mma_bf16_16816(acc[i][2 * jj + 1], a0, a1, a2, a3, bf[jj][2], bf[jj][3]);
+          }
         }
       }
     }
@@ -366,7 +380,7 @@ __device__ __forceinline__ void shrink_bar_all(int bar_id) {
 // One shrink unit (one CTA of its cluster): smem is the 1024-aligned stage pool
 // (kPoolBytes, by default the standalone kernel's sk_pool(kMaxNB16)), bars room
 // for 2 * kSkMaxStages mbarriers and a flag.
-template <int kMaxNB16, int kPoolBytes = sk_pool(kMaxNB16)>
+template <int kMaxNB16, int kPoolBytes = sk_pool(kMaxNB16), bool kFresh = false>
 __device__ __forceinline__ bool shrink_unit(uint8_t *smem, uint64_t *bars, const CUtensorMap &mapIn16,
                                             const CUtensorMap &mapF16, const CUtensorMap &mapBits16,
                                             const ShrinkParams &p, int unit, uint32_t crank, const ShrinkRole role) {
@@ -495,14 +509,14 @@ __device__ __forceinline__ bool shrink_unit(uint8_t *smem, uint64_t *bars, const
     // the piece width nn is 16, 32, 48 or 64 (at most 16 * kMaxNB16: the host
     // launches the small build only for such pieces)
     if constexpr (kMaxNB16 <= 2) {
-      if (g.nn <= 16) shrink_consume<1>(w, p, g, orow, smem, abort_flag, red, warp, lane);
-      else shrink_consume<2>(w, p, g, orow, smem, abort_flag, red, warp, lane);
+      if (g.nn <= 16) shrink_consume<1, kFresh>(w, p, g, orow, smem, abort_flag, red, warp, lane);
+      else shrink_consume<2, kFresh>(w, p, g, orow, smem, abort_flag, red, warp, lane);
     } else {
       switch (g.nn >> 4) {
-        case 1: shrink_consume<1>(w, p, g, orow, smem, abort_flag, red, warp, lane); break;
-        case 2: shrink_consume<2>(w, p, g, orow, smem, abort_flag, red, warp, lane); break;
-        case 3: shrink_consume<3>(w, p, g, orow, smem, abort_flag, red, warp, lane); break;
-        default: shrink_consume<4>(w, p, g, orow, smem, abort_flag, red, warp, lane); break;
+        case 1: shrink_consume<1, kFresh>(w, p, g, orow, smem, abort_flag, red, warp, lane); break;
+        case 2: shrink_consume<2, kFresh>(w, p, g, orow, smem, abort_flag, red, warp, lane); break;
+        case 3: shrink_consume<3, kFresh>(w, p, g, orow, smem, abort_flag, red, warp, lane); break;
+        default: shrink_consume<4, kFresh>(w, p, g, orow, smem, abort_flag, red, warp, lane); break;
       }
     }
   }
@@ -664,7 +678,7 @@ __device__ __forceinline__ bool shrink_unit(uint8_t *smem, uint64_t *bars, const
 
 // Grid: n_units * ksplit CTAs, clusters of ksplit along x. Cluster c handles unit c;
 // its rank q contracts columns [q*kslice, (q+1)*kslice).
-template <int kMaxNB16>
+template <int kMaxNB16, bool kFresh = false>
 __global__ void __launch_bounds__(kSkThreads, sk_ctas_per_sm(kMaxNB16))
     lora_shrink_kernel(const __grid_constant__ CUtensorMap mapIn16,  // In rows (X, sorted X or dY), box {64, 16}
                        const __grid_constant__ CUtensorMap mapF16,   // F rows, box {64, 16}
@@ -674,7 +688,7 @@ __global__ void __launch_bounds__(kSkThreads, sk_ctas_per_sm(kMaxNB16))
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   pdl_launch_dependents();  // the fused GEMM may set itself up meanwhile
-  shrink_unit<kMaxNB16>(smem, reinterpret_cast<uint64_t *>(smem + sk_pool(kMaxNB16)), mapIn16, mapF16, mapBits16, p,
+  shrink_unit<kMaxNB16, sk_pool(kMaxNB16), kFresh>(smem, reinterpret_cast<uint64_t *>(smem + sk_pool(kMaxNB16)), mapIn16, mapF16, mapBits16, p,
                         static_cast<int>(blockIdx.x) / p.ksplit, cluster_ctarank(),
                         ShrinkRole{static_cast<int>(threadIdx.x), 0, true});
 }
