@@ -77,6 +77,10 @@ __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void cp_async16_all(float *dst, const float *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // ------------------------------------------------------------------ momentum
 // m' = beta·m + (1 - beta)·g over the rows of the listed adapters.
 __global__ void __launch_bounds__(256)
@@ -103,9 +107,9 @@ __global__ void __launch_bounds__(256)
 // the eight rows and four columns of a fragment in different banks).
 constexpr int kMuTile = 64;
 constexpr int kMuChunk = 32;
-constexpr int kMuPieceCols = 512;  // columns of one piece of a Gram matrix
+constexpr int kMuPieceCols = 640;  // columns of one piece of a Gram matrix
 constexpr int kMuPitch = kMuChunk + 4;
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
     lora_muon_gram_kernel(const MuonAdapter *__restrict__ ads, const MuonItem *__restrict__ items,
                           const int32_t *__restrict__ active, int64_t d, int64_t piece_cols, MuonInput in,
                           double *__restrict__ partial) {
@@ -119,24 +123,37 @@ __global__ void __launch_bounds__(256)
   const bool diag = it.ti == it.tj;
   double acc[4][4] = {};
   const int64_t c_end = min(d, (it.piece + 1) * piece_cols);
-  for (int64_t c0 = it.piece * piece_cols; c0 < c_end; c0 += kMuChunk) {
-    // 64 rows x 32 columns per operand: 512 float4, two per thread
+  // 64 rows x 32 columns per operand: 512 float4, two per thread; the next chunk's are
+  // on their way while this one is multiplied
+  float4 v[2], w[2];
+  auto fetch = [&](int64_t c0) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int e = threadIdx.x + 256 * u;
       const int row = e >> 3, c4 = (e & 7) * 4;
       const bool in_cols = c0 + c4 < c_end;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f), w = v;
+      v[u] = w[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (in_cols && it.ti * kMuTile + row < ad.rank)
-        v = muon_u4(in, (ad.row0 + it.ti * kMuTile + row) * d + c0 + c4);
-      sa[row][c4] = v.x, sa[row][c4 + 1] = v.y, sa[row][c4 + 2] = v.z, sa[row][c4 + 3] = v.w;
+        v[u] = muon_u4(in, (ad.row0 + it.ti * kMuTile + row) * d + c0 + c4);
+      if (!diag && in_cols && it.tj * kMuTile + row < ad.rank)
+        w[u] = muon_u4(in, (ad.row0 + it.tj * kMuTile + row) * d + c0 + c4);
+    }
+  };
+  fetch(it.piece * piece_cols);
+  for (int64_t c0 = it.piece * piece_cols; c0 < c_end; c0 += kMuChunk) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int e = threadIdx.x + 256 * u;
+      const int row = e >> 3, c4 = (e & 7) * 4;
+      *reinterpret_cast<double2 *>(&sa[row][c4]) = make_double2(v[u].x, v[u].y);
+      *reinterpret_cast<double2 *>(&sa[row][c4 + 2]) = make_double2(v[u].z, v[u].w);
       if (!diag) {
-        if (in_cols && it.tj * kMuTile + row < ad.rank)
-          w = muon_u4(in, (ad.row0 + it.tj * kMuTile + row) * d + c0 + c4);
-        sb[row][c4] = w.x, sb[row][c4 + 1] = w.y, sb[row][c4 + 2] = w.z, sb[row][c4 + 3] = w.w;
+        *reinterpret_cast<double2 *>(&sb[row][c4]) = make_double2(w[u].x, w[u].y);
+        *reinterpret_cast<double2 *>(&sb[row][c4 + 2]) = make_double2(w[u].z, w[u].w);
       }
     }
     __syncthreads();
+    if (c0 + kMuChunk < c_end) fetch(c0 + kMuChunk);
     const double(*pb)[kMuPitch] = diag ? sa : sb;
 #pragma unroll
     for (int k = 0; k < kMuChunk; k += 4) {
@@ -158,7 +175,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The pieces of an adapter's Gram tiles added in order and scaled to G0 =
+// The pieces of an adapter's Gram tiles (a CTA an eighth of a tile) added in order and scaled to G0 =
 // U·U^T / (|U|_F + eps)^2, both triangles, pitch nt·64 (zeros past the rank);
 // |U|_F^2 is the trace. 1 / (|U|_F + eps) goes to inv[ad].
 __global__ void __launch_bounds__(256)
@@ -176,6 +193,7 @@ __global__ void __launch_bounds__(256)
   for (int i = threadIdx.x; i < ad.rank; i += 256) {
     const int ti = i / kMuTile, o = i % kMuTile;
     const int tri = ti * ad.nt - ti * (ti - 1) / 2;
+#pragma unroll 8
     for (int p = 0; p < pieces; ++p)
       tr += partial[ad.pofs + (static_cast<int64_t>(p) * ntri + tri) * kT2 + o * kMuTile + o];
   }
@@ -186,11 +204,12 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
   }
   const double s = 1.0 / (sqrt(red[0]) + kNsEps);
-  if (it.ti == 0 && it.tj == 0 && threadIdx.x == 0) inv[it.ad] = s;
+  if (it.ti == 0 && it.tj == 0 && blockIdx.y == 0 && threadIdx.x == 0) inv[it.ad] = s;
   const int tri = it.ti * ad.nt - it.ti * (it.ti - 1) / 2 + (it.tj - it.ti);
   const int pitch = ad.nt * kMuTile;
-  for (int e = threadIdx.x; e < kT2; e += 256) {
+  for (int e = blockIdx.y * (kT2 / 8) + threadIdx.x; e < static_cast<int>(blockIdx.y + 1) * (kT2 / 8); e += 256) {
     double v = 0.0;
+#pragma unroll 8
     for (int p = 0; p < pieces; ++p) v += partial[ad.pofs + (static_cast<int64_t>(p) * ntri + tri) * kT2 + e];
     v *= s * s;
     const int i = it.ti * kMuTile + e / kMuTile, j = it.tj * kMuTile + e % kMuTile;
@@ -226,15 +245,27 @@ __global__ void __launch_bounds__(128)
   const double *B = p.B + ad.gofs + it.tj * kMuPt * pitch;  // rows of B for its columns: B is symmetric
   double acc[2][4] = {};
   const int kmax = (ad.rank + kMuPt - 1) / kMuPt * kMuPt;
-  for (int k0 = 0; k0 < kmax; k0 += kMuPt) {
+  double2 va[4], vb[4];  // the next chunk, on its way while this one is multiplied
+  auto fetch = [&](int k0) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int e = threadIdx.x + 128 * u;  // 512 double2 per operand
       const int row = e >> 4, c = (e & 15) * 2;
-      *reinterpret_cast<double2 *>(&sa[row][c]) = *reinterpret_cast<const double2 *>(A + row * pitch + k0 + c);
-      *reinterpret_cast<double2 *>(&sb[row][c]) = *reinterpret_cast<const double2 *>(B + row * pitch + k0 + c);
+      va[u] = *reinterpret_cast<const double2 *>(A + row * pitch + k0 + c);
+      vb[u] = *reinterpret_cast<const double2 *>(B + row * pitch + k0 + c);
+    }
+  };
+  fetch(0);
+  for (int k0 = 0; k0 < kmax; k0 += kMuPt) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = threadIdx.x + 128 * u;
+      const int row = e >> 4, c = (e & 15) * 2;
+      *reinterpret_cast<double2 *>(&sa[row][c]) = va[u];
+      *reinterpret_cast<double2 *>(&sb[row][c]) = vb[u];
     }
     __syncthreads();
+    if (k0 + kMuPt < kmax) fetch(k0 + kMuPt);
 #pragma unroll
     for (int k = 0; k < kMuPt; k += 4) {
       const double a0 = sa[mi + g][k + t], a1 = sa[mi + g + 8][k + t];
@@ -287,44 +318,69 @@ __device__ __forceinline__ float muon_step_size(const MuonOutput &o, int rank, i
   return o.rms > 0.f ? o.lr * (o.rms * sqrtf(big)) : o.lr;
 }
 
-// 64 rows x 64 columns of O = P·X0: 256 threads, each 4 x 4, ranks in chunks of 32.
-__global__ void __launch_bounds__(256)
+// 64 rows x 128 columns of O = P·X0: 256 threads, each 8 rows x 4 columns, ranks in
+// chunks of 16, the next chunk on its way while this one is multiplied.
+constexpr int kMuApCols = 128, kMuApK = 16;
+__global__ void __launch_bounds__(256, 2)
     lora_muon_apply_kernel(const MuonAdapter *__restrict__ ads, const MuonItem *__restrict__ items,
                            const int32_t *__restrict__ active, int64_t d, MuonInput in, const double *__restrict__ P,
                            const double *__restrict__ inv, MuonOutput out) {
   const MuonItem it = items[blockIdx.x];
   const MuonAdapter ad = ads[it.ad];
   if (active && active[ad.index] == 0) return;
-  __shared__ float sp[32][kMuTile + 4];  // P^T: [k][row]
-  __shared__ __align__(16) float su[32][kMuTile];
+  __shared__ __align__(16) float sp[kMuApK][kMuTile];    // P^T: [k][row]
+  __shared__ __align__(16) float su[kMuApK][kMuApCols];
   const int64_t pitch = ad.nt * kMuTile;
   const double s = inv[it.ad];
-  const int tr = (threadIdx.x >> 4) * 4, tc = (threadIdx.x & 15) * 4;
-  float acc[4][4] = {};
-  const int64_t c0 = static_cast<int64_t>(it.piece) * kMuTile;
-  for (int k0 = 0; k0 < ad.rank; k0 += 32) {
-    for (int e = threadIdx.x; e < 32 * kMuTile; e += 256) {
-      // P is symmetric: row k of P holds column k
-      const int k = e / kMuTile, i = e % kMuTile;
-      sp[k][i] = static_cast<float>(P[ad.gofs + (k0 + k) * pitch + it.ti * kMuTile + i] * s);
+  const int64_t c0 = static_cast<int64_t>(it.piece) * kMuApCols;
+  // a warp: 8 rows, its lanes the 32 groups of 4 columns
+  const int tr = (threadIdx.x >> 5) * 8, tc = (threadIdx.x & 31) * 4;
+  float4 acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  double pv[4];
+  float4 uv[2];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = threadIdx.x + 256 * u;
+      // P is symmetric: row k of P holds column k (zero past the rank within its tiles of 32)
+      pv[u] = P[ad.gofs + (k0 + e / kMuTile) * pitch + it.ti * kMuTile + e % kMuTile];
     }
-    for (int e = threadIdx.x; e < 32 * kMuTile / 4; e += 256) {
-      const int k = e / (kMuTile / 4), c = (e % (kMuTile / 4)) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k0 + k < ad.rank && c0 + c < d) v = muon_u4(in, (ad.row0 + k0 + k) * d + c0 + c);
-      *reinterpret_cast<float4 *>(&su[k][c]) = v;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int e = threadIdx.x + 256 * u;
+      const int k = e >> 5, c = (e & 31) * 4;
+      uv[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k < ad.rank && c0 + c < d) uv[u] = muon_u4(in, (ad.row0 + k0 + k) * d + c0 + c);
+    }
+  };
+  fetch(0);
+  for (int k0 = 0; k0 < ad.rank; k0 += kMuApK) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int e = threadIdx.x + 256 * u;
+      sp[e / kMuTile][e % kMuTile] = static_cast<float>(pv[u] * s);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int e = threadIdx.x + 256 * u;
+      *reinterpret_cast<float4 *>(&su[e >> 5][(e & 31) * 4]) = uv[u];
     }
     __syncthreads();
+    if (k0 + kMuApK < ad.rank) fetch(k0 + kMuApK);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
+    for (int k = 0; k < kMuApK; ++k) {
       const float4 u = *reinterpret_cast<const float4 *>(&su[k][tc]);
+      const float4 p0 = *reinterpret_cast<const float4 *>(&sp[k][tr]);
+      const float4 p1 = *reinterpret_cast<const float4 *>(&sp[k][tr + 4]);
+      const float av[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = sp[k][tr + i];
-        acc[i][0] = fmaf(a, u.x, acc[i][0]);
-        acc[i][1] = fmaf(a, u.y, acc[i][1]);
-        acc[i][2] = fmaf(a, u.z, acc[i][2]);
-        acc[i][3] = fmaf(a, u.w, acc[i][3]);
+      for (int i = 0; i < 8; ++i) {
+        acc[i].x = fmaf(av[i], u.x, acc[i].x);
+        acc[i].y = fmaf(av[i], u.y, acc[i].y);
+        acc[i].z = fmaf(av[i], u.z, acc[i].z);
+        acc[i].w = fmaf(av[i], u.w, acc[i].w);
       }
     }
     __syncthreads();
@@ -332,10 +388,9 @@ __global__ void __launch_bounds__(256)
   const float step = muon_step_size(out, ad.rank, d);
   if (c0 + tc < d) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const int row = it.ti * kMuTile + tr + i;
-      if (row < ad.rank)
-        muon_store4(out, (ad.row0 + row) * d + c0 + tc, step, make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]));
+      if (row < ad.rank) muon_store4(out, (ad.row0 + row) * d + c0 + tc, step, acc[i]);
     }
   }
 }
@@ -559,8 +614,16 @@ __global__ void __launch_bounds__(256, MuF<NB>::kCtas)
   const int nc4 = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(p.slice), p.d - c0)) / 4);
   const int64_t base = ad.row0 * p.d + c0;
 
-  // ---- the slice's rows: momentum, U
-  {
+  // ---- the slice's rows: momentum, U; where U is an input, straight to its place
+  // (cp.async, all in flight at once)
+  if (!p.m) {
+    for (int e = threadIdx.x; e < r * nc4; e += 256) {
+      const int row = e / nc4, c = 4 * (e - row * nc4);
+      cp_async16_all(us + row * p.slice + (c ^ ((row & 7) << 2)), p.g + base + row * p.d + c);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else {
     constexpr int kUn = F::kUn;
     const int total = r * nc4;
     int row = 0, c = static_cast<int>(threadIdx.x);
@@ -578,7 +641,7 @@ __global__ void __launch_bounds__(256, MuF<NB>::kCtas)
         if (e0 + 256 * u < total) {
           const int64_t o = base + row * p.d + 4 * c;
           gv[u] = *reinterpret_cast<const float4 *>(p.g + o);
-          if (p.m) mv[u] = *reinterpret_cast<const float4 *>(p.m + o);
+          mv[u] = *reinterpret_cast<const float4 *>(p.m + o);
         }
         c += 256;
         while (c >= nc4) {
@@ -590,21 +653,19 @@ __global__ void __launch_bounds__(256, MuF<NB>::kCtas)
       for (int u = 0; u < kUn; ++u) {
         if (e0 + 256 * u < total) {
           float4 v = gv[u];
-          if (p.m) {
-            float4 m = mv[u];
-            m.x = fmaf(p.beta, m.x, p.omb * v.x);
-            m.y = fmaf(p.beta, m.y, p.omb * v.y);
-            m.z = fmaf(p.beta, m.z, p.omb * v.z);
-            m.w = fmaf(p.beta, m.w, p.omb * v.w);
-            *reinterpret_cast<float4 *>(p.m_out + base + rr[u] * p.d + 4 * cc[u]) = m;
-            if (p.nesterov) {
-              v.x = fmaf(p.beta, m.x, p.omb * v.x);
-              v.y = fmaf(p.beta, m.y, p.omb * v.y);
-              v.z = fmaf(p.beta, m.z, p.omb * v.z);
-              v.w = fmaf(p.beta, m.w, p.omb * v.w);
-            } else {
-              v = m;
-            }
+          float4 m = mv[u];
+          m.x = fmaf(p.beta, m.x, p.omb * v.x);
+          m.y = fmaf(p.beta, m.y, p.omb * v.y);
+          m.z = fmaf(p.beta, m.z, p.omb * v.z);
+          m.w = fmaf(p.beta, m.w, p.omb * v.w);
+          *reinterpret_cast<float4 *>(p.m_out + base + rr[u] * p.d + 4 * cc[u]) = m;
+          if (p.nesterov) {
+            v.x = fmaf(p.beta, m.x, p.omb * v.x);
+            v.y = fmaf(p.beta, m.y, p.omb * v.y);
+            v.z = fmaf(p.beta, m.z, p.omb * v.z);
+            v.w = fmaf(p.beta, m.w, p.omb * v.w);
+          } else {
+            v = m;
           }
           *reinterpret_cast<float4 *>(us + rr[u] * p.slice + ((4 * cc[u]) ^ ((rr[u] & 7) << 2))) = v;
         }
