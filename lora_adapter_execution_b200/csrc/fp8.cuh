@@ -71,6 +71,8 @@ constexpr int kQRowsWarps = 8;
 __global__ void __launch_bounds__(32 * kQRowsWarps)
     lora_fp8_rows_kernel(const uint16_t *__restrict__ X, const int32_t *__restrict__ perm, int64_t T, int64_t d,
                          uint8_t *__restrict__ Q, float *__restrict__ S, uint16_t *__restrict__ Xs) {
+  pdl_wait();
+  pdl_launch_dependents();  // the next kernel may set itself up meanwhile (never before the last one is done)
   const int lane = threadIdx.x & 31;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kQRowsCols + lane * 8;
   for (int64_t i = static_cast<int64_t>(blockIdx.y) * kQRowsWarps + (threadIdx.x >> 5); i < T;
@@ -102,6 +104,8 @@ __global__ void __launch_bounds__(256)
     lora_gather_set_kernel(const int32_t *__restrict__ perm, int64_t T, const uint4 *__restrict__ X, uint4 *Xs,
                            int x_row, const uint4 *__restrict__ B, uint4 *Bs, int b_row, const float *__restrict__ U,
                            float *Us, int r, int rp) {
+  pdl_wait();
+  pdl_launch_dependents();
   // a warp per row
   const int lane = threadIdx.x & 31;
   const int64_t nw = static_cast<int64_t>(gridDim.x) * 8;
@@ -223,6 +227,8 @@ struct Fp8Params {
   const float *Sx;  // [K blocks][T]: scale of A's row i (in A's row order) in K block b
   const float *Sw;  // scale of weight block (K block b, column block j) at b * sw_k + j * sw_n
   int32_t sw_k, sw_n, n_nb;  // n_nb: column blocks
+  int32_t a_bytes;  // bytes of an A copy: the whole tile, or only the rows that a short batch has
+                    // (the other rows' products are whatever the stage held, and are not used)
 };
 
 // D[tmem] (+)= A·B, e4m3 operands, fp32 accumulation, K = 32.
@@ -333,7 +339,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait();  // every operand may come from the kernel before this one
+  // Every operand may come from the kernel before this one. The next kernel is not let
+  // in early: lora_gemm_kernel reads its W before it waits, and W may be this output.
+  pdl_wait();
 
   const int n_tiles = p.n_mt * p.n_nt;
   const int KB = (p.K + kF8K - 1) / kF8K;
@@ -368,7 +376,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             const uint32_t b_dst = a_dst + kF8StageA;
             const uint32_t fb = full0 + 8 * stage;
             if (blk < KB) {
-              mbar_arrive_expect_tx(fb, C::kStage);
+              mbar_arrive_expect_tx(fb, static_cast<uint32_t>(fp.a_bytes) + C::kStageB);
               tma_load_2d(a_dst, &mapA, fb, blk * kF8K, td.row0);
               if (B_KMAJOR) {
                 tma_load_2d(b_dst, &mapB, fb, blk * kF8K, n0);

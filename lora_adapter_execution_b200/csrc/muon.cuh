@@ -455,6 +455,7 @@ struct MuonFused {
   int nesterov;
   int64_t d;
   int slice;            // columns per CTA, a multiple of 32
+  int more;             // another launch of this step follows
 };
 
 // One tile of A·B for symmetric commuting operands, of which the 16 x 16 blocks on
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(256, MuF<NB>::kCtas)
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank_in));
   // the launches of one step work on different adapters: the next one may start
   // once all of this one's CTAs run, and none ends before the one before it has
-  pdl_launch_dependents();
+  if (p.more) pdl_launch_dependents();
   const MuonAdapter ad = ads[blockIdx.x / ncta];
   if (active && active[ad.index] == 0) {  // the whole cluster
     pdl_wait();
