@@ -403,3 +403,100 @@ def test_layer_two_streams_two_plans():
     torch.cuda.synchronize()
     for a, b in zip(alone, got):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_workspace_too_small_and_out_of_place_arguments():
+    inp = layer(20, 64, 48, [4], np.zeros(20, np.int32), 0.0)
+    plan = lora.Plan(inp.ids, inp.ranks, 64, 48)
+    X, A, B = dev_bf16(inp.X), dev_bf16(inp.A_pool), dev_bf16(inp.B_pool)
+    Wq, Sw = torch.zeros(64, 48, device="cuda").to(FP8), torch.ones(1, 1, device="cuda")
+    Y, sc = torch.empty(20, 48, dtype=torch.bfloat16, device="cuda"), torch.ones(1, device="cuda")
+    need = lora.fwd_fp8_workspace_size(plan)
+    big = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    for ws in (big[:need - 1], big[16:16 + need]):  # one byte short; not 256-byte aligned
+        with pytest.raises(lora.LoraError) as e:
+            lora.linear_fwd_fp8(plan, X, Wq, Sw, A, B, sc, Y, ws)
+        assert e.value.code == -8
+    with pytest.raises(lora.LoraError) as e:
+        lora.linear_fwd_fp8(plan, X, Wq, Sw, A, B, sc, Y, big, p_drop=1.0)
+    assert e.value.code == -1
+    lora.linear_fwd_fp8(plan, X, Wq, Sw, A, B, sc, Y, big[:need])
+    assert lora.device_status() == 0
+    plan.destroy()
+
+
+def test_offsets_past_32_bits():
+    """Rows whose bytes lie past 2^31 and elements past 2^31: the last rows equal the same rows alone."""
+    T, d = 270000, 8192
+    g = torch.Generator(device="cuda").manual_seed(3)
+    tail = torch.randn(300, d, generator=g, device="cuda").to(torch.bfloat16)
+    X = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    X[-300:] = tail
+    Q, S = torch.empty(T, d, dtype=torch.uint8, device="cuda"), torch.empty(blocks(d), T, device="cuda")
+    lora.quantize_rows(X, Q, S)
+    Qt, St = quantize_rows(tail)
+    assert torch.equal(Q[-300:], Qt.view(torch.uint8)) and torch.equal(S[:, -300:], St)
+    assert (Q[:100] == 0).all() and (S[:, :100] == 1).all()
+    del X
+    Wq = torch.randn(d, 16, generator=g, device="cuda").to(FP8)
+    Sw = torch.ones(blocks(d), 1, device="cuda")
+    Y = torch.empty(T, 16, dtype=torch.bfloat16, device="cuda")
+    lora.base_gemm_fp8(Q, S, Wq, Sw, Y)
+    assert lora.device_status() == 0
+    W, Xv = f64(Wq), rows_value(f64(Qt), f64(St))
+    ref, mag = Xv @ W, np.abs(Xv) @ np.abs(W)
+    assert (np.abs(f64(Y[-300:]) - ref) <= 2.0**-8 * np.abs(ref) + (2.0**-21 + (blocks(d) + 3) * 2.0**-24) * mag).all()
+    assert (Y[:100] == 0).all()
+
+
+def test_fine_tuning_steps_over_an_8_bit_base():
+    """The pieces as they are used: quantise the base once; per step the forward, a
+    gradient of the output, the backward, a Muon step of both pools in place, the next
+    step reading the bf16 pools. The first step's gradients and updates equal the
+    formulas' in 64 bits, adapters without tokens stay as they were, and further steps run."""
+    T, di, do, ranks = 200, 256, 384, [8, 3, 16, 21]
+    rng = np.random.default_rng(8)
+    ids = rng.integers(0, 3, size=T).astype(np.int32)  # adapter 3 has no token
+    inp = layer(T, di, do, ranks, ids, 0.0, seed=9)
+    dev, bf = "cuda", torch.bfloat16
+    plan = lora.Plan(ids, ranks, di, do)
+    X, W = dev_bf16(inp.X), dev_bf16(inp.W)
+    Wq, Sw = torch.empty(di, do, dtype=FP8, device=dev), torch.empty(blocks(di), blocks(do), device=dev)
+    lora.quantize_weight(W, Wq, Sw)
+    scale = torch.from_numpy(inp.scale).to(dev)
+    pools = [dev_bf16(inp.A_pool), dev_bf16(inp.B_pool)]
+    masters = [p.float() for p in pools]
+    moms = [torch.zeros_like(m) for m in masters]
+    muons = [lora.Muon(ranks, di), lora.Muon(ranks, do)]
+    active = torch.tensor([1, 1, 1, 0], dtype=torch.int32, device=dev)
+    Y, U = torch.empty(T, do, dtype=bf, device=dev), torch.empty(T, plan.r_max, device=dev)
+    dX, grads = torch.empty(T, di, dtype=bf, device=dev), [torch.full_like(m, float("nan")) for m in masters]
+    ws = torch.empty(max(lora.fwd_fp8_workspace_size(plan), lora.bwd_multi_fp8_workspace_size(plan)), dtype=torch.uint8,
+                     device=dev)
+    dY = dev_bf16(inp.dY)
+    before = [m.clone() for m in masters]
+    lr, rms = 0.05, 0.2
+    for step in range(3):
+        lora.linear_fwd_fp8(plan, X, Wq, Sw, *pools, scale, Y, ws, U_save=U)
+        lora.linear_bwd_multi_fp8(plan, X, Wq, Sw, *pools, scale, U, dY, dX, *grads, ws)
+        for mu, g, m, w, p in zip(muons, grads, moms, masters, pools):
+            mu.step(g, m, w, pool=p, lr=lr, beta=0.0, rms=rms, active=active)
+        assert lora.device_status() == 0
+        if step == 0:
+            rY, rdX, rdA, rdB = ref_layer(inp)
+            check_close(host_f64(Y), rY, "Y")
+            check_close(host_f64(dX), rdX, "dX")
+            for w, b, rg in zip(masters, before, (rdA, rdB)):
+                for a in range(3):
+                    r = slice(int(inp.offsets[a]), int(inp.offsets[a + 1]))
+                    x = rg[r] / np.linalg.norm(rg[r])
+                    for _ in range(5):
+                        G = x @ x.T
+                        x = 3.4445 * x + (-4.7750 * G + 2.0315 * G @ G) @ x
+                    want = f64(b)[r] - lr * rms * np.sqrt(max(ranks[a], w.shape[1])) * x
+                    check_close(f64(w)[r], want, f"adapter {a}")
+    last = slice(int(inp.offsets[3]), int(inp.offsets[4]))
+    for w, b, p, m in zip(masters, before, pools, moms):
+        assert torch.equal(w[last], b[last]) and torch.equal(p[last], b[last].to(bf)) and (m[last] == 0).all()
+        assert torch.isfinite(w).all() and torch.equal(p, w.to(bf)) and not torch.equal(w, b)
+    plan.destroy()

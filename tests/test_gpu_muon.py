@@ -231,3 +231,38 @@ def test_refuses_overlap():
                dict(momentum_out=t[3], master_out=t[3])):
         with pytest.raises(lora.LoraError):
             mu.step(t[0], t[1], t[2], lr=0.1, **kw)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^31 elements: its last adapters equal the same rows alone."""
+    d, n = 8192, 16500
+    ranks = [16] * n + [70]
+    U = torch.zeros(sum(ranks), d, device="cuda")
+    assert U.numel() > 2**31
+    tail = pools([16, 16, 70], d, seed=9)(1.0)
+    U[-102:] = tail
+    O = torch.empty_like(U)
+    lora.Muon(ranks, d).orthogonalize(U, O)
+    assert lora.device_status() == 0
+    alone = torch.empty_like(tail)
+    lora.Muon([16, 16, 70], d).orthogonalize(tail, alone)
+    assert torch.equal(O[-102:], alone)
+    assert (O[:1000] == 0).all()
+
+
+def test_two_contexts_on_two_streams():
+    ranks, d = [24, 7, 64, 130], 1024
+    Us = [pools(ranks, d, seed=20 + i)(1.0) for i in range(2)]
+    mus = [lora.Muon(ranks, d) for _ in Us]
+    alone = [torch.empty_like(u) for u in Us]
+    for m, u, o in zip(mus, Us, alone):
+        m.orthogonalize(u, o)
+    torch.cuda.synchronize()
+    both = [torch.empty_like(u) for u in Us]
+    streams = [torch.cuda.Stream() for _ in Us]
+    for _ in range(3):
+        for st, m, u, o in zip(streams, mus, Us, both):
+            m.orthogonalize(u, o, stream=st)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert torch.equal(a, b)
