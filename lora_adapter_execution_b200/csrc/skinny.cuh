@@ -688,7 +688,8 @@ __global__ void __launch_bounds__(kSkThreads, sk_ctas_per_sm(kMaxNB16))
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   pdl_launch_dependents();  // the fused GEMM may set itself up meanwhile
-  shrink_unit<kMaxNB16, sk_pool(kMaxNB16), kFresh>(smem, reinterpret_cast<uint64_t *>(smem + sk_pool(kMaxNB16)), mapIn16, mapF16, mapBits16, p,
+  shrink_unit<kMaxNB16, sk_pool(kMaxNB16), kFresh>(smem, reinterpret_cast<uint64_t *>(smem + sk_pool(kMaxNB16)),
+                                                   mapIn16, mapF16, mapBits16, p,
                         static_cast<int>(blockIdx.x) / p.ksplit, cluster_ctarank(),
                         ShrinkRole{static_cast<int>(threadIdx.x), 0, true});
 }
