@@ -77,7 +77,7 @@ __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ void cp_async16_all(float *dst, const float *src) {
+__device__ __forceinline__ void cp_async16_all(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(256)
 // each 16 x 32. Columns in chunks of 32, as doubles in shared memory (pitch 36:
 // the eight rows and four columns of a fragment in different banks). Bound by the fp64
 // tensor MMAs (64 multiply-adds a cycle and SM): 6 adapters of 256 x 4096 need 57 us of
-// them; the whole orthogonalisation takes 332 us (419 without the chunk ahead).
+// them; the pass takes 95, the whole orthogonalisation 332 us (308 in a graph; one chunk
+// at a time: 419).
 constexpr int kMuTile = 64;
 constexpr int kMuChunk = 32;
 constexpr int kMuPieceCols = 640;  // columns of one piece of a Gram matrix
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(256, 3)
                           double *__restrict__ partial) {
   const MuonItem it = items[blockIdx.x];
   const MuonAdapter ad = ads[it.ad];
+  pdl_launch_dependents();  // (launched the ordinary way: all before it is done)
   if (active && active[ad.index] == 0) return;
   __shared__ double sa[kMuTile][kMuPitch], sb[kMuTile][kMuPitch];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -177,29 +179,59 @@ __global__ void __launch_bounds__(256, 3)
   }
 }
 
-// The pieces of an adapter's Gram tiles (a CTA an eighth of a tile) added in order and scaled to G0 =
-// U·U^T / (|U|_F + eps)^2, both triangles, pitch nt·64 (zeros past the rank);
-// |U|_F^2 is the trace. 1 / (|U|_F + eps) goes to inv[ad].
+// The launches from here to the application are short and each reads what the one
+// before it wrote. They may be launched with programmatic serialization: they read their
+// tables meanwhile and then wait, every CTA of them, so that the end of one launch means
+// the end of all before it; the application, the last, lets nothing start early.
+
+// kN values of a Gram tile, v[i] = the sum of its pieces at `at + i·step`, added in order,
+// four pieces' loads in flight.
+template <int kN>
+__device__ __forceinline__ void muon_sum_pieces(double (&v)[kN], const double *at, int64_t step, int64_t stride,
+                                                int pieces) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = 0.0;
+  for (int p = 0; p < pieces; p += 4) {
+    double x[4][kN];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < kN; ++i) x[q][i] = p + q < pieces ? at[(p + q) * stride + i * step] : 0.0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] += x[q][i];
+  }
+}
+
+// The pieces of an adapter's Gram tiles (a CTA an eighth of a tile) added in order and
+// scaled to G0 = U·U^T / (|U|_F + eps)^2, both triangles, pitch nt·64 (zeros past the
+// rank); |U|_F^2 is the trace. 1 / (|U|_F + eps) goes to inv[ad].
 __global__ void __launch_bounds__(256)
     lora_muon_reduce_kernel(const MuonAdapter *__restrict__ ads, const MuonItem *__restrict__ items,
                             const int32_t *__restrict__ active, int pieces, const double *__restrict__ partial,
                             double *__restrict__ G, double *__restrict__ inv) {
   const MuonItem it = items[blockIdx.x];
   const MuonAdapter ad = ads[it.ad];
+  pdl_wait();
+  pdl_launch_dependents();
   if (active && active[ad.index] == 0) return;
   const int ntri = ad.nt * (ad.nt + 1) / 2;
   constexpr int kT2 = kMuTile * kMuTile;
   __shared__ double red[256];
-  // the trace, the same way in every CTA of the adapter
-  double tr = 0.0;
-  for (int i = threadIdx.x; i < ad.rank; i += 256) {
-    const int ti = i / kMuTile, o = i % kMuTile;
+  const int64_t stride = static_cast<int64_t>(ntri) * kT2;  // from piece to piece
+  // the trace, the same way in every CTA of the adapter (rank <= 256: a thread a term)
+  double tr[1] = {0.0};
+  if (static_cast<int>(threadIdx.x) < ad.rank) {
+    const int i = threadIdx.x, ti = i / kMuTile, o = i % kMuTile;
     const int tri = ti * ad.nt - ti * (ti - 1) / 2;
-#pragma unroll 8
-    for (int p = 0; p < pieces; ++p)
-      tr += partial[ad.pofs + (static_cast<int64_t>(p) * ntri + tri) * kT2 + o * kMuTile + o];
+    muon_sum_pieces(tr, partial + ad.pofs + static_cast<int64_t>(tri) * kT2 + o * kMuTile + o, 0, stride, pieces);
   }
-  red[threadIdx.x] = tr;
+  const int tri = it.ti * ad.nt - it.ti * (it.ti - 1) / 2 + (it.tj - it.ti);
+  const int e0 = blockIdx.y * (kT2 / 8) + threadIdx.x;
+  double v[2];
+  muon_sum_pieces(v, partial + ad.pofs + static_cast<int64_t>(tri) * kT2 + e0, 256, stride, pieces);
+  red[threadIdx.x] = tr[0];
   __syncthreads();
   for (int o = 128; o > 0; o >>= 1) {
     if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
@@ -207,88 +239,90 @@ __global__ void __launch_bounds__(256)
   }
   const double s = 1.0 / (sqrt(red[0]) + kNsEps);
   if (it.ti == 0 && it.tj == 0 && blockIdx.y == 0 && threadIdx.x == 0) inv[it.ad] = s;
-  const int tri = it.ti * ad.nt - it.ti * (it.ti - 1) / 2 + (it.tj - it.ti);
   const int pitch = ad.nt * kMuTile;
-  for (int e = blockIdx.y * (kT2 / 8) + threadIdx.x; e < static_cast<int>(blockIdx.y + 1) * (kT2 / 8); e += 256) {
-    double v = 0.0;
-#pragma unroll 8
-    for (int p = 0; p < pieces; ++p) v += partial[ad.pofs + (static_cast<int64_t>(p) * ntri + tri) * kT2 + e];
-    v *= s * s;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int e = e0 + 256 * u;
+    const double x = v[u] * (s * s);
     const int i = it.ti * kMuTile + e / kMuTile, j = it.tj * kMuTile + e % kMuTile;
-    G[ad.gofs + static_cast<int64_t>(i) * pitch + j] = v;
-    if (it.ti != it.tj) G[ad.gofs + static_cast<int64_t>(j) * pitch + i] = v;
+    G[ad.gofs + static_cast<int64_t>(i) * pitch + j] = x;
+    if (it.ti != it.tj) G[ad.gofs + static_cast<int64_t>(j) * pitch + i] = x;
   }
 }
 
 // ------------------------------------------------------------------ r x r products
-// One 32 x 32 tile (ti <= tj in units of 32) of C = A·B for symmetric commuting
-// matrices (so C is symmetric: the tile and its mirror are written); `poly`:
+// One half, 32 x 16, of a 32 x 32 tile (ti <= tj in units of 32) of C = A·B for symmetric
+// commuting matrices (so C is symmetric: the tile and its mirror are written); `poly`:
 // C = a·I + b·A + c·A·B instead (A = B = G gives Q). Up to two products per launch
-// (blockIdx.y). 4 warps, each 16 x 16; K in chunks of 32.
+// (blockIdx.y). 4 warps, each 16 x 8 in four chains of MMAs (by k), added at the end; K in
+// chunks of 32, three of them on their way by cp.async.
 struct MuonProduct {
   const double *A, *B;
   double *C;
   int poly;
 };
 constexpr int kMuPt = 32;
+constexpr int kMuPtStages = 4;
+constexpr int kMuPtRows = kMuPt + kMuPt / 2;  // rows of A and B in a stage
+constexpr int kMuPtSmem = kMuPtStages * kMuPtRows * kMuPitch * 8;
 __global__ void __launch_bounds__(128)
     lora_muon_product_kernel(const MuonAdapter *__restrict__ ads, const MuonItem *__restrict__ items,
                              const int32_t *__restrict__ active, MuonProduct p0, MuonProduct p1) {
-  const MuonItem it = items[blockIdx.x];
+  const MuonItem it = items[blockIdx.x >> 1];
   const MuonAdapter ad = ads[it.ad];
+  pdl_wait();
+  pdl_launch_dependents();
   if (active && active[ad.index] == 0) return;
   const MuonProduct p = blockIdx.y ? p1 : p0;
-  __shared__ double sa[kMuPt][kMuPitch], sb[kMuPt][kMuPitch];
+  extern __shared__ __align__(16) double mu_stages[];  // [stage][A's 32 rows, B's 16][kMuPitch]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int mi = (warp & 1) * 16, nj = (warp >> 1) * 16;
+  const int mi = (warp & 1) * 16, nj = (warp >> 1) * 8;
+  const int half = (blockIdx.x & 1) * (kMuPt / 2);
   const int64_t pitch = ad.nt * kMuTile;
   const double *A = p.A + ad.gofs + it.ti * kMuPt * pitch;
-  const double *B = p.B + ad.gofs + it.tj * kMuPt * pitch;  // rows of B for its columns: B is symmetric
-  double acc[2][4] = {};
+  const double *B = p.B + ad.gofs + (it.tj * kMuPt + half) * pitch;  // rows of B for its columns: B is symmetric
+  double acc[4][4] = {};
   const int kmax = (ad.rank + kMuPt - 1) / kMuPt * kMuPt;
-  double2 va[4], vb[4];  // the next chunk, on its way while this one is multiplied
-  auto fetch = [&](int k0) {
+  const int chunks = kmax / kMuPt;
+  auto fetch = [&](int c) {  // one group a chunk, empty past the last
+    if (c < chunks) {
+      double *st = mu_stages + (c % kMuPtStages) * (kMuPtRows * kMuPitch);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = threadIdx.x + 128 * u;  // 512 double2 per operand
-      const int row = e >> 4, c = (e & 15) * 2;
-      va[u] = *reinterpret_cast<const double2 *>(A + row * pitch + k0 + c);
-      vb[u] = *reinterpret_cast<const double2 *>(B + row * pitch + k0 + c);
+      for (int u = 0; u < 6; ++u) {
+        const int e = threadIdx.x + 128 * u;  // 512 pairs of A, 256 of B
+        const int row = e >> 4, k = (e & 15) * 2;
+        cp_async16_all(st + row * kMuPitch + k, (u < 4 ? A + row * pitch : B + (row - kMuPt) * pitch) + c * kMuPt + k);
+      }
     }
+    cp_async_commit();
   };
-  fetch(0);
-  for (int k0 = 0; k0 < kmax; k0 += kMuPt) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int e = threadIdx.x + 128 * u;
-      const int row = e >> 4, c = (e & 15) * 2;
-      *reinterpret_cast<double2 *>(&sa[row][c]) = va[u];
-      *reinterpret_cast<double2 *>(&sb[row][c]) = vb[u];
-    }
-    __syncthreads();
-    if (k0 + kMuPt < kmax) fetch(k0 + kMuPt);
+  for (int c = 0; c < kMuPtStages - 1; ++c) fetch(c);
+  for (int c = 0; c < chunks; ++c) {
+    cp_async_wait<kMuPtStages - 2>();
+    __syncthreads();  // chunk c is here, and all are done with chunk c - 1, whose stage is filled next
+    fetch(c + kMuPtStages - 1);
+    const double(*sa)[kMuPitch] =
+        reinterpret_cast<const double(*)[kMuPitch]>(mu_stages + (c % kMuPtStages) * (kMuPtRows * kMuPitch));
+    const double(*sb)[kMuPitch] = sa + kMuPt;
 #pragma unroll
     for (int k = 0; k < kMuPt; k += 4) {
       const double a0 = sa[mi + g][k + t], a1 = sa[mi + g + 8][k + t];
-      dmma(acc[0], a0, a1, sb[nj + g][k + t]);
-      dmma(acc[1], a0, a1, sb[nj + 8 + g][k + t]);
+      dmma(acc[(k >> 2) & 3], a0, a1, sb[nj + g][k + t]);
     }
-    __syncthreads();
   }
   double *C = p.C + ad.gofs;
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = it.ti * kMuPt + mi + g + (e >> 1) * 8;
-      const int col = it.tj * kMuPt + nj + 8 * j + 2 * t + (e & 1);
-      double v = acc[j][e];
-      if (p.poly)
-        v = kNsCd * v + kNsBd * p.A[ad.gofs + row * pitch + col] + (row == col && row < ad.rank ? kNsAd : 0.0);
-      C[row * pitch + col] = v;
-      if (it.ti != it.tj) C[col * pitch + row] = v;
-    }
+  for (int e = 0; e < 4; ++e) {
+    const int row = it.ti * kMuPt + mi + g + (e >> 1) * 8;
+    const int col = it.tj * kMuPt + half + nj + 2 * t + (e & 1);
+    double v = (acc[0][e] + acc[1][e]) + (acc[2][e] + acc[3][e]);
+    if (p.poly)
+      v = kNsCd * v + kNsBd * p.A[ad.gofs + row * pitch + col] + (row == col && row < ad.rank ? kNsAd : 0.0);
+    C[row * pitch + col] = v;
+    if (it.ti != it.tj) C[col * pitch + row] = v;
+  }
 }
 
 // ------------------------------------------------------------------ application
@@ -321,7 +355,9 @@ __device__ __forceinline__ float muon_step_size(const MuonOutput &o, int rank, i
 }
 
 // 64 rows x 128 columns of O = P·X0: 256 threads, each 8 rows x 4 columns, ranks in
-// chunks of 16, the next chunk on its way while this one is multiplied.
+// chunks of 16, the next chunk on its way while this one is multiplied. Six 256 x 4096:
+// 94 us, half the fp32 rate (8 x 8 per thread, two multiply-adds to an instruction and two
+// buffers in shared memory, singly and together, took 94 to 97 us).
 constexpr int kMuApCols = 128, kMuApK = 16;
 __global__ void __launch_bounds__(256, 2)
     lora_muon_apply_kernel(const MuonAdapter *__restrict__ ads, const MuonItem *__restrict__ items,
@@ -329,6 +365,7 @@ __global__ void __launch_bounds__(256, 2)
                            const double *__restrict__ inv, MuonOutput out) {
   const MuonItem it = items[blockIdx.x];
   const MuonAdapter ad = ads[it.ad];
+  pdl_wait();
   if (active && active[ad.index] == 0) return;
   __shared__ __align__(16) float sp[kMuApK][kMuTile];    // P^T: [k][row]
   __shared__ __align__(16) float su[kMuApK][kMuApCols];
