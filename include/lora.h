@@ -28,8 +28,8 @@
  *    host arrays (and its forward scratch) until lora_plan_destroy.
  *  - Every call that launches work is asynchronous and ordered on `stream`
  *    (a cudaStream_t; NULL is the legacy default stream). Nothing synchronises
- *    the host except lora_plan_build (which copies the plan to the device) and
- *    lora_device_status.
+ *    the host except lora_plan_build and lora_muon_create (which copy tables to
+ *    the device) and lora_device_status.
  *  - Return value: LORA_OK (0) or a negative LORA_ERR_* code. Arguments are
  *    validated on the host before any launch; on an error nothing is launched.
  *    No exception crosses the ABI.
@@ -639,7 +639,8 @@ int lora_linear_bwd_multi_fp8(lora_plan_t plan, const uint16_t *X, const uint8_t
  *
  * lora_muon_create — a context for pools of one shape.
  *   ranks_host  int32[n_adapters]: 1 .. LORA_MAX_RANK
- *   d           the rows' length, a multiple of 8, >= 8 (d_in for A_pool, d_out for B_pool)
+ *   d           the rows' length, a multiple of 8, >= 8 (d_in for A_pool, d_out for B_pool);
+ *               R·d <= 2^40, R the sum of the ranks
  * It owns device tables and scratch, copies them to the device (the call waits
  * for that) and belongs to the device current at this call. Two calls with one
  * context must be ordered (they share its scratch), two captured graphs' replays
