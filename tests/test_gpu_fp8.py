@@ -500,3 +500,53 @@ def test_fine_tuning_steps_over_an_8_bit_base():
         assert torch.equal(w[last], b[last]) and torch.equal(p[last], b[last].to(bf)) and (m[last] == 0).all()
         assert torch.isfinite(w).all() and torch.equal(p, w.to(bf)) and not torch.equal(w, b)
     plan.destroy()
+
+
+@pytest.mark.parametrize("runs", [False, True])  # tokens of an adapter together, or scattered
+def test_a_captured_step_replays_as_the_eager_one(runs):
+    """Forward, backward and the Muon step of one pool in one graph, replayed over new
+    inputs in the same buffers: bit for bit the eager calls' results."""
+    T, di, do, ranks = 300, 384, 272, [8, 33, 16, 70]
+    rng = np.random.default_rng(12)
+    ids = rng.integers(0, 4, size=T).astype(np.int32)
+    ids = np.sort(ids) if runs else ids
+    inp = layer(T, di, do, ranks, ids, 0.1, seed=13)
+    bf, dev = torch.bfloat16, "cuda"
+    plan = lora.Plan(ids, ranks, di, do)
+    X, A, B, dY = dev_bf16(inp.X), dev_bf16(inp.A_pool), dev_bf16(inp.B_pool), dev_bf16(inp.dY)
+    Wq, Sw = torch.empty(di, do, dtype=FP8, device=dev), torch.empty(blocks(di), blocks(do), device=dev)
+    lora.quantize_weight(dev_bf16(inp.W), Wq, Sw)
+    scale = torch.from_numpy(inp.scale).to(dev)
+    mu = lora.Muon(ranks, di)
+    mom, master = torch.randn(A.shape, device=dev), A.float()
+    ws = torch.empty(max(lora.fwd_fp8_workspace_size(plan), lora.bwd_multi_fp8_workspace_size(plan)), dtype=torch.uint8,
+                     device=dev)
+
+    def buffers():
+        return [torch.zeros(T, do, dtype=bf, device=dev), torch.zeros(T, plan.r_max, device=dev),
+                torch.zeros(T, di, dtype=bf, device=dev), torch.zeros(A.shape, device=dev),
+                torch.zeros(B.shape, device=dev), torch.zeros_like(mom), torch.zeros_like(master), torch.zeros_like(A)]
+
+    def step(o):
+        Y, U, dX, dA, dB, m2, w2, pool = o
+        lora.linear_fwd_fp8(plan, X, Wq, Sw, A, B, scale, Y, ws, U_save=U, p_drop=0.1, seed=5)
+        lora.linear_bwd_multi_fp8(plan, X, Wq, Sw, A, B, scale, U, dY, dX, dA, dB, ws, p_drop=0.1, seed=5)
+        mu.step(dA, mom, master, m2, w2, pool, lr=0.02)
+
+    eager, captured = buffers(), buffers()
+    step(eager)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(captured)
+    for k in range(3):
+        if k:
+            X.mul_(-2)
+            dY.mul_(0.5)
+            step(eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert lora.device_status() == 0
+        for e, c in zip(eager, captured):
+            assert torch.equal(e, c)
+    plan.destroy()
