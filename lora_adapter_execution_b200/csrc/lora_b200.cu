@@ -1374,8 +1374,10 @@ int bwd_multi_run(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const 
   const float inv_keep = p_drop > 0.0 ? static_cast<float>(1.0 / (1.0 - p_drop)) : 1.0f;
   const uint32_t *bits = thr ? keep_bits : nullptr;
   // keep bits for the dA contraction: rows in the order of its In rows (sorted
-  // when the plan gathers), staged through TMA when rows are 16-byte multiples
-  const bool bits_tc = bits && wpr % 4 == 0;
+  // when the plan gathers), staged through TMA when the array and its rows lie on
+  // 16-byte boundaries (the gather moves 16 bytes at a time, too); else the contraction
+  // derives them from the generator
+  const bool bits_tc = bits && wpr % 4 == 0 && aligned16(bits);
   const uint32_t *bits_in = gathers && bits_tc ? reinterpret_cast<const uint32_t *>(ws + Lw.bits) : bits;
 
   auto grid_for = [&](int64_t n) {

@@ -550,3 +550,45 @@ def test_a_captured_step_replays_as_the_eager_one(runs):
         for e, c in zip(eager, captured):
             assert torch.equal(e, c)
     plan.destroy()
+
+
+@pytest.mark.parametrize("runs", [False, True])  # tokens of an adapter together, or scattered
+def test_keep_bits_of_four_byte_alignment(runs):
+    """Keep bits may start at any 4-byte boundary: forward and backward over both bases give
+    what they give with the same bits on a 16-byte one."""
+    T, di, do, ranks, p, seed = 200, 256, 272, [8, 21], 0.3, 11
+    ids = np.arange(T, dtype=np.int32) % 2
+    ids = np.sort(ids) if runs else ids
+    inp = layer(T, di, do, ranks, ids, p, seed=21)
+    dev, bf = "cuda", torch.bfloat16
+    plan = lora.Plan(ids, ranks, di, do)
+    X, W, A, B, dY = (dev_bf16(v) for v in (inp.X, inp.W, inp.A_pool, inp.B_pool, inp.dY))
+    Wq, Sw = torch.empty(di, do, dtype=FP8, device=dev), torch.empty(blocks(di), blocks(do), device=dev)
+    lora.quantize_weight(W, Wq, Sw)
+    scale = torch.from_numpy(inp.scale).to(dev)
+    ws = torch.empty(max(lora.fwd_fp8_workspace_size(plan), lora.bwd_multi_fp8_workspace_size(plan)), dtype=torch.uint8,
+                     device=dev)
+    room = torch.empty(T * (di // 32) + 4, dtype=torch.int32, device=dev)
+
+    def results(shift):
+        bits = room[shift:shift + T * (di // 32)].view(T, di // 32)
+        assert bits.data_ptr() % 16 == 4 * shift
+        lora.dropout_keep_bits(seed, p, bits, di)
+        kw = dict(p_drop=p, seed=seed, keep_bits=bits)
+        out = []
+        for fwd, bwd, base in ((lora.linear_fwd_fp8, lora.linear_bwd_multi_fp8, (Wq, Sw)),
+                               (lora.linear_fwd, lora.linear_bwd_multi, (W,))):
+            Y, U = torch.empty(T, do, dtype=bf, device=dev), torch.empty(T, plan.r_max, device=dev)
+            dX = torch.empty(T, di, dtype=bf, device=dev)
+            dA, dB = torch.zeros(A.shape, device=dev), torch.zeros(B.shape, device=dev)
+            fwd(plan, X, *base, A, B, scale, Y, *([ws] if len(base) == 2 else []), U_save=U, **kw)
+            bwd(plan, X, *base, A, B, scale, U, dY, dX, dA, dB, ws, **kw)
+            assert lora.device_status() == 0
+            out += [Y, U, dX, dA, dB]
+        return out
+
+    want = results(0)
+    for shift in (1, 2, 3):
+        for a, b in zip(want, results(shift)):
+            assert torch.equal(a, b)
+    plan.destroy()

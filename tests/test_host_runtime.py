@@ -50,3 +50,45 @@ def test_muon_create_waits_for_its_tables(lib):
     assert lib.lora_muon_create(ranks.ctypes.data_as(vp), 3, ctypes.c_int64(512), ctypes.byref(mu)) == 0
     assert lib.fake_pending() == 0
     lib.lora_muon_destroy(mu)
+
+
+def built_plan(lib, T=64, d_in=256, d_out=128, ranks=(4, 8)):
+    """A plan whose tokens are scattered over its adapters (so rows are gathered)."""
+    ids, ranks = np.arange(T, dtype=np.int32) % len(ranks), np.array(ranks, np.int32)
+    plan = vp()
+    assert lib.lora_plan_build(ids.ctypes.data_as(vp), ctypes.c_int64(T), ranks.ctypes.data_as(vp), len(ranks),
+                               ctypes.c_int64(d_in), ctypes.c_int64(d_out), None, ctypes.byref(plan)) == 0
+    lib.fake_clear()
+    return plan
+
+
+def launches(lib):
+    return [(lib.fake_launch_name(i).decode(), [lib.fake_launch_arg(i, k) for k in range(lib.fake_launch_args(i))])
+            for i in range(lib.fake_launches())]
+
+
+P = vp(0x10000)  # stands for an aligned device array: nothing reads it
+BIG = ctypes.c_size_t(1 << 30)
+
+
+def backward(lib, plan, eight_bit, keep_bits):
+    zero = ctypes.c_uint64(5)
+    base = (P, P) if eight_bit else (P,)
+    fn = lib.lora_linear_bwd_multi_fp8 if eight_bit else lib.lora_linear_bwd_multi
+    return fn(plan, P, *base, P, P, P, ctypes.c_double(0.1), zero, P, P, P, P, P, P, BIG, keep_bits, None)
+
+
+@pytest.mark.parametrize("eight_bit", [False, True])
+def test_keep_bits_of_four_byte_alignment(lib, eight_bit):
+    """Keep bits need 4-byte alignment only: the kernels that gather rows in pieces of 16
+    bytes get no other address."""
+    plan = built_plan(lib)
+    for bits in (0x20000, 0x20004, 0x20008):
+        lib.fake_clear()
+        assert backward(lib, plan, eight_bit, vp(bits)) == 0
+        gathers = [a for n, a in launches(lib) if "lora_gather_" in n and a]
+        assert gathers
+        sources = [a[5] if len(a) == 6 else a[0] for a in gathers]
+        assert all(s % 16 == 0 for s in sources), (hex(bits), sources)
+        assert (bits in sources) == (bits % 16 == 0)
+    lib.lora_plan_destroy(plan)
