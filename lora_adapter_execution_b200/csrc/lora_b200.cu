@@ -32,6 +32,9 @@ struct DeviceState {
   // the fused forward's cooperative launch: most CTAs resident at once in
   // clusters of S = 1, 2, 4 (index S)
   int fz_max_ctas[5] = {0, 0, 0, 0, 0};
+  // attributes of the 8-bit layer's and the Muon step's kernels: what fails there
+  // refuses their calls alone (family_state)
+  bool fp8_ok = false, muon_ok = false;
 };
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -84,18 +87,13 @@ int device_state(DeviceState **out) {
                                      sk_smem(4)) == cudaSuccess;
           ok &= cudaFuncSetAttribute(lora_shrink_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      sk_smem(2)) == cudaSuccess;
-          ok &= cudaFuncSetAttribute(lora_shrink_kernel<4, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     sk_smem(4)) == cudaSuccess;
-          ok &= cudaFuncSetAttribute(lora_shrink_kernel<2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     sk_smem(2)) == cudaSuccess;
           ok &= cudaFuncSetAttribute(lora_tcontract_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      tc_smem(kTcMaxR)) == cudaSuccess;
-          ok &= cudaFuncSetAttribute(lora_tcontract_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     tc_smem(kTcMaxR)) == cudaSuccess;
           ok &= qr_kernel_attributes();
-          ok &= fp8_kernel_attributes();
-          ok &= muon_kernel_attributes();
           if (!ok) d.status = LORA_ERR_CUDA;
+          d.fp8_ok = fp8_kernel_attributes();
+          d.muon_ok = muon_kernel_attributes();
+          if (!d.fp8_ok || !d.muon_ok) cudaGetLastError();
           for (int S = 1; ok && S <= 4; S *= 2) {
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(static_cast<unsigned>(S));
@@ -122,6 +120,12 @@ int device_state(DeviceState **out) {
   }
   *out = &d;
   return d.status;
+}
+
+// device_state for a call that launches kernels of one family.
+int family_state(DeviceState **out, bool DeviceState::*family_ok) {
+  const int rc = device_state(out);
+  return rc != LORA_OK || (*out)->*family_ok ? rc : LORA_ERR_CUDA;
 }
 
 // 2-D bf16 tensor map over a row-major [rows x cols] matrix.
@@ -1354,7 +1358,7 @@ int bwd_multi_run(lora_plan_t plan, const uint16_t *X, const uint16_t *W, const 
   if (!workspace || workspace_bytes < workspace_need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return LORA_ERR_WORKSPACE;
   DeviceState *ds = nullptr;
-  int rc = device_state(&ds);
+  int rc = f8 ? family_state(&ds, &DeviceState::fp8_ok) : device_state(&ds);
   if (rc != LORA_OK) return rc;
 
   const int64_t T = hp.T, d_in = hp.d_in, d_out = hp.d_out;

@@ -92,3 +92,35 @@ def test_keep_bits_of_four_byte_alignment(lib, eight_bit):
         assert all(s % 16 == 0 for s in sources), (hex(bits), sources)
         assert (bits in sources) == (bits % 16 == 0)
     lib.lora_plan_destroy(plan)
+
+
+def test_a_short_register_count_refuses_the_8_bit_product_alone(lib):
+    """A build whose 8-bit product got too few registers for its split (it would wait for
+    them for ever) refuses the calls that launch that product, before any launch, and
+    no other."""
+    lib.fake_set_regs(160)
+    n = ctypes.c_int64
+    assert lib.lora_base_gemm(P, P, P, n(64), n(256), n(128), None) == 0
+    assert lib.lora_fp8_quantize_rows(P, n(64), n(256), P, P, None) == 0
+    assert lib.lora_fp8_quantize_weight(P, n(256), n(128), P, P, None) == 0
+    ranks = np.array([4, 70, 16], np.int32)
+    mu = vp()
+    assert lib.lora_muon_create(ranks.ctypes.data_as(vp), 3, n(512), ctypes.byref(mu)) == 0
+    assert lib.lora_muon_orthogonalize(mu, P, vp(0x1000000), None, None) == 0
+    lib.lora_muon_destroy(mu)
+    plan = built_plan(lib)
+    assert backward(lib, plan, False, None) == 0
+    lib.fake_clear()
+    CUDA = -4
+    assert lib.lora_base_gemm_fp8(P, P, P, P, P, n(64), n(256), n(128), 0, None) == CUDA
+    assert lib.lora_linear_fwd_fp8(plan, P, P, P, P, P, P, ctypes.c_double(0.0), ctypes.c_uint64(0), P, P, P, BIG, None,
+                                   None) == CUDA
+    assert backward(lib, plan, True, None) == CUDA
+    assert launches(lib) == []
+    lib.lora_plan_destroy(plan)
+
+
+def test_enough_registers_launch_the_8_bit_product(lib):
+    n = ctypes.c_int64
+    assert lib.lora_base_gemm_fp8(P, P, P, P, P, n(64), n(256), n(128), 0, None) == 0
+    assert [name for name, _ in launches(lib) if "lora_fp8_gemm_kernel" in name]
