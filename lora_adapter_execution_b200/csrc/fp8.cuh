@@ -310,12 +310,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const uint32_t fixed0 = empty0 + 8 * C::kStages;    // [kStages] released by the fix-up warp
   const uint32_t accf0 = fixed0 + 8 * C::kStages;     // [kBuf]
   const uint32_t acce0 = accf0 + 8 * C::kBuf;         // [kBuf]
-  uint32_t *words = reinterpret_cast<uint32_t *>(bars + 3 * C::kStages + 2 * C::kBuf);
+  const uint32_t done0 = acce0 + 8 * C::kBuf;         // [2] after a wait gave up: an issuing warp's MMAs are done
+  uint32_t *words = reinterpret_cast<uint32_t *>(bars + 3 * C::kStages + 2 * C::kBuf + 2);
   uint32_t *tmem_slot = words;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(words + 1);
-  volatile uint32_t *bmap = words + 2;                   // [kStages] slot of each K step of an adapter block
-  volatile uint32_t *bvalid = words + 2 + C::kStages;    // [kStages] AugBlockDesc::valid | nslot << 20
-  static_assert((3 * C::kStages + 2 * C::kBuf) * 8 + (2 + 2 * C::kStages) * 4 <= C::kBars, "barrier block");
+  volatile uint32_t *filled = words + 2;                 // where the copying thread ended: its phase · kStages + its stage
+  volatile uint32_t *bmap = words + 3;                   // [kStages] slot of each K step of an adapter block
+  volatile uint32_t *bvalid = words + 3 + C::kStages;    // [kStages] AugBlockDesc::valid | nslot << 20
+  static_assert((3 * C::kStages + 2 * C::kBuf + 2) * 8 + (3 + 2 * C::kStages) * 4 <= C::kBars, "barrier block");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -329,7 +331,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       mbar_init(accf0 + 8 * b, 1);
       mbar_init(acce0 + 8 * b, kF8Sum / 32);  // one arrival per accumulating warp
     }
+    mbar_init(done0, 1);
+    mbar_init(done0 + 8, 1);
     *abort_flag = 0;
+    *filled = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -352,6 +357,25 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   const int q = S > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int tile0 = static_cast<int>(blockIdx.x) / S;
   const int tile_step = S > 1 ? n_tiles : static_cast<int>(gridDim.x);
+  // After a wait gave up (every warp has joined): what is in flight ends, each wait
+  // bounded too, before TMEM is freed and shared memory given up.
+  auto settle = [&]() {
+    if (warp == 1 || warp == 2) {
+      if (elect_one()) umma_commit(done0 + 8 * (warp - 1));
+      __syncwarp();
+    }
+    if (warp == 1) {
+      mbar_wait(done0, 0);
+      mbar_wait(done0 + 8, 0);
+      __syncwarp();
+    }
+    if (threadIdx.x == 0) {
+      // the last copy into each stage: in this phase before the stage where the copying
+      // ended, in the one before from there on (never filled: that phase counts as done)
+      const uint32_t end = *filled % C::kStages, ph = *filled / C::kStages;
+      for (uint32_t s = 0; s < C::kStages; ++s) mbar_wait(full0 + 8 * s, s < end ? ph : ph ^ 1);
+    }
+  };
 
   if (warp < 4) {
     if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kF8RegsCopy));
@@ -410,6 +434,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             if (++stage == C::kStages) { stage = 0; phase ^= 1; }
           }
         }
+        *filled = phase * C::kStages + stage;
       }
     } else if (warp == 3) {
       // ------------------------------------------------ fix-up (see gemm.cuh): with a
@@ -535,6 +560,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     if constexpr (BN == 256) {
       tc_fence_before();
       f8_join();  // every TMEM read is done
+      if (*abort_flag) settle();
       if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, 512);
@@ -586,7 +612,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       auto drain = [&](int e, auto add) -> bool {
         const uint32_t n = (rings >> (8 * e)) & 0xFFu;
         const int buf = e + 2 * (n % (C::kBuf / 2));
-        if (!mbar_wait(accf0 + 8 * buf, (n / (C::kBuf / 2)) & 1u)) { *abort_flag = 1; return false; }
+        // (agreed by the warp: what follows is for whole warps)
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(accf0 + 8 * buf, (n / (C::kBuf / 2)) & 1u))) {
+          *abort_flag = 1;
+          return false;
+        }
         tc_fence_after();
         const uint32_t ta = lane_base + buf * BN;
         if (quarter * 32 < td.rows) {  // (a warp without rows has nothing to add)
@@ -676,6 +706,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if constexpr (BN == 128) {
     tc_fence_before();
     f8_join();
+    if (*abort_flag) settle();
     if (warp == 1) {
       __syncwarp();
       tc_fence_after();
