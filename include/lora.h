@@ -579,7 +579,9 @@ int lora_fp8_quantize_weight(const uint16_t *W, int64_t d_in, int64_t d_out, uin
  *                 Xq [T, d_out], Sx [ceil(d_out/128), T], Y bf16 [T, d_in]
  *   Wq [d_in, d_out], Sw [ceil(d_in/128), ceil(d_out/128)]; d_in, d_out
  *   multiples of 16, >= 16. Sx and Sw may hold any fp32 values (those of
- *   lora_fp8_quantize_* or of a checkpoint).
+ *   lora_fp8_quantize_* or of a checkpoint). The product of two scales that meet is
+ *   formed in fp32: outside fp32's normal numbers it has fewer bits (below 2^-126) or
+ *   is infinite, and so are the results.
  * Each block's product is formed in fp32 and added, scaled, to fp32 sums; one
  * rounding to bf16. The order of the sums is fixed: results are the same run to
  * run. Xq, Wq, Y 16-byte aligned, Sx, Sw 4-byte aligned.
@@ -654,6 +656,8 @@ int lora_linear_bwd_multi_fp8(lora_plan_t plan, const uint16_t *X, const uint8_t
  *           are left out, no output row of theirs is written (adapters without
  *           tokens in the batch, whose gradient rows the backward leaves as they
  *           were)
+ * P / |u|_F, with which the rows are multiplied in the end, is held in fp32: for norms
+ * above 2^126 (8.5e37) it has fewer than 24 bits.
  * All arrays 16-byte aligned (active 4). Rows are read and written in fp32; a
  * non-finite value in an adapter's rows makes that adapter's results NaN, no other's.
  * Errors: LORA_ERR_ARG, LORA_ERR_RANK, LORA_ERR_NOMEM, LORA_ERR_UNSUPPORTED, LORA_ERR_CUDA.

@@ -592,3 +592,23 @@ def test_keep_bits_of_four_byte_alignment(runs):
         for a, b in zip(want, results(shift)):
             assert torch.equal(a, b)
     plan.destroy()
+
+
+@pytest.mark.parametrize("ex,ew", [(-60, -60), (100, 5), (-126, 100), (120, -140), (-145, 120)])
+@pytest.mark.parametrize("T,di,do", [(8, 512, 256), (300, 512, 8192)])  # split K; wide tiles
+def test_product_scales_at_the_ends_of_fp32(T, di, do, ex, ew):
+    """Scales at either end of fp32's range, subnormal ones among them, whose products are
+    normal numbers: as exact as others. A scale's own bits below fp32's are taken from
+    the tensor, so subnormal scales are what they are."""
+    g = torch.Generator(device="cuda").manual_seed(T + ex)
+    Xq = torch.randn(T, di, generator=g, device="cuda").mul(100).clamp(-448, 448).to(FP8)
+    Wq = torch.randn(di, do, generator=g, device="cuda").mul(100).clamp(-448, 448).to(FP8)
+    wide = lambda *s, e: ((torch.rand(*s, generator=g, device="cuda", dtype=torch.float64) + 1) * 2.0**e).float()
+    Sx, Sw = wide(blocks(di), T, e=ex), wide(blocks(di), blocks(do), e=ew)
+    Y = torch.empty(T, do, dtype=torch.bfloat16, device="cuda")
+    lora.base_gemm_fp8(Xq, Sx, Wq, Sw, Y)
+    assert lora.device_status() == 0
+    X, W = rows_value(f64(Xq), f64(Sx)), weight_value(f64(Wq), f64(Sw))
+    ref, mag = X @ W, np.abs(X) @ np.abs(W)
+    tol = 2.0**-8 * np.abs(ref) + (2.0**-21 + (blocks(di) + 3) * 2.0**-24) * mag
+    assert (np.abs(f64(Y) - ref) <= tol).all()
