@@ -612,3 +612,58 @@ def test_product_scales_at_the_ends_of_fp32(T, di, do, ex, ew):
     ref, mag = X @ W, np.abs(X) @ np.abs(W)
     tol = 2.0**-8 * np.abs(ref) + (2.0**-21 + (blocks(di) + 3) * 2.0**-24) * mag
     assert (np.abs(f64(Y) - ref) <= tol).all()
+
+
+class Prepared:
+    """A layer's plan, inputs, outputs and workspace, made beforehand, so that run() only queues."""
+
+    def __init__(self, inp):
+        dev, bf = "cuda", torch.bfloat16
+        self.plan = lora.Plan(inp.ids, inp.ranks, inp.d_in, inp.d_out)
+        self.X, W, self.A, self.B, self.dY = (dev_bf16(v) for v in (inp.X, inp.W, inp.A_pool, inp.B_pool, inp.dY))
+        self.Wq = torch.empty(W.shape, dtype=FP8, device=dev)
+        self.Sw = torch.empty(blocks(inp.d_in), blocks(inp.d_out), device=dev)
+        lora.quantize_weight(W, self.Wq, self.Sw)
+        self.scale = torch.from_numpy(inp.scale).to(dev)
+        self.ws = torch.empty(max(lora.fwd_fp8_workspace_size(self.plan), lora.bwd_multi_fp8_workspace_size(self.plan)),
+                              dtype=torch.uint8, device=dev)
+        self.kw = dict(p_drop=inp.p_drop, seed=inp.mask_seed)
+        self.new_outputs = lambda: [torch.zeros(inp.T, inp.d_out, dtype=bf, device=dev),
+                                    torch.zeros(inp.T, self.plan.r_max, device=dev),
+                                    torch.zeros(inp.T, inp.d_in, dtype=bf, device=dev),
+                                    torch.zeros(self.A.shape, device=dev), torch.zeros(self.B.shape, device=dev)]
+
+    def run(self, out):
+        Y, U, dX, dA, dB = out
+        base = (self.Wq, self.Sw, self.A, self.B, self.scale)
+        lora.linear_fwd_fp8(self.plan, self.X, *base, Y, self.ws, U_save=U, **self.kw)
+        lora.linear_bwd_multi_fp8(self.plan, self.X, *base, U, self.dY, dX, dA, dB, self.ws, **self.kw)
+
+
+def test_layers_overlap_on_two_streams_and_in_a_graph():
+    """Forwards and backwards of two layers queued alternately on two streams, and a third
+    layer's replayed graph beside them, nothing waited for in between: the serial bits."""
+    shapes = [(900, 1024, 768, [8, 16, 70]), (700, 768, 1040, [21, 5]), (64, 2048, 512, [16, 4, 33])]
+    layers = [Prepared(layer(T, di, do, r, np.arange(T) % len(r), 0.1, seed=30 + i))
+              for i, (T, di, do, r) in enumerate(shapes)]
+    want, got = ([l.new_outputs() for l in layers] for _ in range(2))
+    for l, o in zip(layers, want):
+        l.run(o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layers[2].run(got[2])
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                layers[k].run(got[k])
+        with torch.cuda.stream(streams[2]):
+            graph.replay()
+    torch.cuda.synchronize()
+    assert lora.device_status() == 0
+    for w, g in zip(want, got):
+        for a, b in zip(w, g):
+            assert torch.equal(a, b)
+    for l in layers:
+        l.plan.destroy()
