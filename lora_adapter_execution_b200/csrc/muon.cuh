@@ -106,11 +106,16 @@ __global__ void __launch_bounds__(256)
 // each 16 x 32. Columns in chunks of 32, as doubles in shared memory (pitch 36:
 // the eight rows and four columns of a fragment in different banks). Bound by the fp64
 // tensor MMAs (64 multiply-adds a cycle and SM): 6 adapters of 256 x 4096 need 57 us of
-// them; the pass takes 95, the whole orthogonalisation 332 us (308 in a graph; one chunk
-// at a time: 419).
+// them; the whole orthogonalisation takes 334 us (301 in a graph; one chunk at a time: 419).
 constexpr int kMuTile = 64;
 constexpr int kMuChunk = 32;
-constexpr int kMuPieceCols = 640;  // columns of one piece of a Gram matrix
+// Columns of one piece of a Gram matrix: short ones spread a few adapters over the SMs,
+// long ones leave fewer partial tiles (32 KB each) to store and add. Whole
+// orthogonalisations in a graph, us, pieces of 256 / 384 / 512 / 640 / 1024: one
+// 96 x 1024 73 / 81 / 87 / 95 / 117, one 256 x 4096 113 / 115 / 124 / 132 / 158, six of them
+// 300 / 301 / 307 / 302 / 316, seven 349 / 355 / 360 / 363 / 356, six 256 x 11008 562 / 556 /
+// 550 / 562 / 568, fifty 64 x 11008 391 / 382 / 382 / 378 / 404.
+constexpr int kMuPieceCols = 384;
 constexpr int kMuPitch = kMuChunk + 4;
 __global__ void __launch_bounds__(256, 3)
     lora_muon_gram_kernel(const MuonAdapter *__restrict__ ads, const MuonItem *__restrict__ items,
