@@ -13,9 +13,11 @@ barrier and a device synchronisation, repeated until the clock sampler has
 seen it for a while, and the median region is reported (max over ranks).
 
 With no --config every workload runs in one process and rank 0 prints ONE
-JSON line: the fine-tuning workload (the largest single-GPU configuration,
-forward + backward) is the headline (`value`, `roofline`, `e2e`,
-`cpu_baseline`), and `configs` holds the same record for every workload.
+JSON line (short: below 2000 characters): the fine-tuning workload (the largest
+single-GPU configuration, forward + backward) is the headline (`value`,
+`roofline`, `e2e`, `cpu_baseline`), and `configs` holds every workload's value,
+milliseconds a step, end-to-end value and roofline fraction. The whole record of
+every workload goes to standard error, a line each.
 `roofline` is the fused forward GEMM (the kernel the layer is built around),
 timed alone in short bursts against the burst peak; `layer_roofline` is the
 whole step, timed over long back-to-back regions, against the sustained peak.
@@ -1224,8 +1226,44 @@ def measure_compress(cx, cpu_budget):
 
 
 HEAD_KEYS = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better", "scaling",
-             "vs_baseline", "dtype", "data", "config", "timing", "roofline", "layer_roofline", "gpu_launches",
-             "clocks", "layer", "e2e", "cpu_baseline")
+             "vs_baseline", "dtype", "data", "config", "gpu_launches")
+# what the printed line keeps of the records within a workload's record
+SUB_KEYS = {"e2e": ("value", "unit", "h2d_bytes_per_step", "d2h_bytes_per_step"),
+            "clocks": ("sm_mhz", "sm_max_mhz", "reasons"),
+            "roofline": ("bound", "achieved", "peak", "unit", "frac", "traffic"),
+            "layer_roofline": ("frac",),
+            "cpu_baseline": ("value", "unit", "cores", "kind")}
+CONFIG_COLUMNS = ("value", "ms_per_step", "e2e", "roofline_frac")
+LINE_MAX = 2000  # characters of the printed line: readers keep the end of the output only
+
+
+def _digits(v, n=6):
+    """Floats to n significant digits, in any nesting."""
+    if isinstance(v, float) and math.isfinite(v):
+        v = float(f"{v:.{n}g}")
+        return int(v) if v.is_integer() and abs(v) < 1e15 else v
+    if isinstance(v, dict):
+        return {k: _digits(x, n) for k, x in v.items()}
+    if isinstance(v, (list, tuple)):
+        return [_digits(x, n) for x in v]
+    return v
+
+
+def result_line(headline, entries):
+    """The printed line: the headline workload's record without its explanations and, with
+    several workloads, a row of CONFIG_COLUMNS for each."""
+    head = entries[headline]
+    out = {k: head[k] for k in HEAD_KEYS if k in head}
+    for k, keep in SUB_KEYS.items():
+        if isinstance(head.get(k), dict):
+            out[k] = {x: head[k][x] for x in keep if x in head[k]}
+    if len(entries) > 1:
+        out["headline"] = headline
+        out["configs"] = {"columns": list(CONFIG_COLUMNS)}
+        for name, e in entries.items():
+            out["configs"][name] = _digits([e.get("value"), e.get("ms_per_step"), (e.get("e2e") or {}).get("value"),
+                                            (e.get("roofline") or {}).get("frac")], 4)
+    return json.dumps(_digits(out))
 
 
 def run_lora(a):
@@ -1241,13 +1279,10 @@ def run_lora(a):
         entries["switch"] = measure_switch(cx, CPU_BUDGET_S["other"])
         entries["factor_qr"] = measure_tsqr(cx, CPU_BUDGET_S["other"])
         entries["compress"] = measure_compress(cx, CPU_BUDGET_S["other"])
-    head = entries[HEADLINE if a.config == "all" else a.config]
-    out = {k: head[k] for k in HEAD_KEYS if k in head}
-    if a.config == "all":
-        out["headline"] = f"{HEADLINE} (the largest single-GPU configuration); every workload under configs"
-        out["configs"] = entries
     if cx.rank == 0:
-        print(json.dumps(out), flush=True)
+        for name, e in entries.items():
+            print(f"{name}: {json.dumps(e)}", file=sys.stderr, flush=True)
+        print(result_line(HEADLINE if a.config == "all" else a.config, entries), flush=True)
     if cx.world > 1:
         import torch.distributed as dist
         dist.barrier()
