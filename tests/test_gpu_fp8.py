@@ -667,3 +667,37 @@ def test_layers_overlap_on_two_streams_and_in_a_graph():
             assert torch.equal(a, b)
     for l in layers:
         l.plan.destroy()
+
+
+@pytest.mark.parametrize("case", range(len(LAYERS)))
+def test_layer_outputs_to_their_rounding(case):
+    """Y and dX element by element. Each is rounded once to bf16 (2^-8). The base term is the
+    product's (see above). The adapter term is s·U (or s·dU) times the pool's rows: U is
+    summed to (2^-21 + (d/16 + 4)·2^-24) of its terms' magnitudes (see test_U_to_fp32),
+    s·U is held as two bf16 parts, each rounded to half a step (2^-8 · 2^-8 = 2^-16 left
+    over), and its products are summed by MMAs in fp32, 16 ranks an MMA (2^-21 of the
+    magnitudes each time, ranks to 256 in two parts: 32 of them at most, 2^-16)."""
+    T, di, do, ranks, ids, p = LAYERS[case]
+    inp = layer(T, di, do, ranks, ids(T), p, seed=case)
+    Y, _, dX, _, _ = run_layer(inp)
+    b = wl.bf16_bits_to_f32
+    X, W, A, B, dY = (b(v).astype(np.float64) for v in (inp.X, inp.W, inp.A_pool, inp.B_pool, inp.dY))
+    W = weight_value(*ref_weight(W))
+    keep = np.ones((T, di))
+    if p > 0:
+        keep = (1 - oracle.mask(inp.mask_seed, p, T, di)) / (1 - p)
+    for got, rows, w, first, second, masked_in in ((Y, X, W, A, B, True), (dX, dY, W.T, B, A, False)):
+        k = rows.shape[1]
+        xq = rows_value(*ref_rows(rows))
+        ref, tol = xq @ w, (2.0**-21 + (blocks(k) + 3) * 2.0**-24) * (np.abs(xq) @ np.abs(w))
+        for a in range(inp.n_adapters):
+            t = np.flatnonzero(inp.ids == a)
+            r, sc = slice(int(inp.offsets[a]), int(inp.offsets[a + 1])), float(inp.scale[a])
+            x = rows[t] * keep[t] if masked_in else rows[t]
+            m = 1.0 if masked_in else keep[t]
+            u, mag = sc * x @ first[r].T, sc * np.abs(x) @ np.abs(first[r]).T
+            ref[t] += m * (u @ second[r])
+            tol[t] += m * ((2.0**-16 + 2.0**-16) * np.abs(u) @ np.abs(second[r])
+                           + (2.0**-21 + (k / 16 + 4) * 2.0**-24) * mag @ np.abs(second[r]))
+        tol += 2.0**-8 * (np.abs(ref) + tol)
+        assert (np.abs(f64(got) - ref) <= tol).all(), (np.abs(f64(got) - ref) / tol).max()
