@@ -175,10 +175,22 @@ __global__ void __launch_bounds__(256)
 // about 1,100 cycles a block beside everything else: warp 1 + e takes the stages of
 // parity e and fills TMEM buffers of its own. A tile's adapter blocks therefore end
 // in up to two buffers (those on even stages, those on odd ones), drained before
-// the base blocks'. What bounds it: the loads in flight (4 stages of 48 KB) against
-// their latency, 760 cycles a block where the MMAs take 512, and the hand-over of
-// the buffers. 5003 x 11008 x 4096: 263 us, 1.72 PFLOP/s (one issuing warp, scales
-// loaded a block ahead: 373 us; a pair of CTAs on 256 rows, cta_group::2: 277 us).
+// the base blocks'. What bounds it: a block of 128 takes about 1070 cycles (5003 x
+// 11008 x 4096 under ncu: 461,182 for the longest CTA's five tiles of 86 blocks), its
+// MMAs 512 of them. Loads alone, free-running (4 stages of 48 KB), took 760, the
+// hand-over of the buffers alone 608: they add up more than they overlap. Which of the
+// path from L2 (39 bytes a cycle and SM are reached) and the shared memory port holds
+// the loads was not measured. And tiles come in whole rounds: 640 of them on 148 CTAs
+// are five rounds for 4.32 (592 tiles, four rounds: 232 us, 640: 290). 5003 x 11008 x 4096:
+// 268 us under ncu, 1.69 PFLOP/s, 285 in a graph over three sets of operands (one issuing
+// warp, scales loaded a block ahead: a third slower; a pair of CTAs on 256 rows,
+// cta_group::2: 5 % slower).
+//
+// The adapters' s·U (s·dU) comes as two bf16 parts, hi + lo, 16 bits (the image that
+// lora_shrink_kernel writes for the bf16 layer, too): a third part would make half as
+// many adapter blocks again. What it costs before the rounding to bf16 is 2.3e-6 of the
+// output's norm (the fleet's dX; measured against 64 bits), where that rounding itself
+// is 1.7e-3: one output in 700 becomes its bf16 neighbour.
 constexpr int kF8Groups = 2;                   // accumulating warpgroups
 constexpr int kF8Sum = 128 * kF8Groups;        // accumulating threads
 constexpr int kF8Threads = 128 + kF8Sum;

@@ -10,8 +10,9 @@
 //   Q = a·I + b·G + c·G·G;   P <- P·Q;   G <- Q·G·Q      (all of them commute)
 //
 // Precision. A step multiplies a small singular value by a = 3.4445, so it grows
-// a^2 = 12-fold in G per step, and so does any error G has there: an error of
-// 2^-24 of |G| in G0 would be 5000 times as large by the fifth step. The Gram matrix and
+// a^2 = 11.86-fold in G per step, and so does any error G has there: 11.86^4 = 2e4-fold
+// before the fifth step, and in the result the largest slope of P(g)·sqrt(g), 3.6e4 (at
+// singular values of 0.004): an error of 2^-24 of |G| in G0 would be 2e-3 there. The Gram matrix and
 // the r x r matrices are therefore held and multiplied in 64 bits (fp64 tensor
 // MMAs); P is rounded once, to fp32, for the product with X0, whose own
 // terms are fp32.
